@@ -171,6 +171,11 @@ kara_status decode_impl(const void* q, const void* k_new, const void* v_new, con
   return launch_decode(L, stream);
 }
 
+bool new_slots_ok(const kara_pool* pool, int32_t new_slots) {
+  return new_slots >= 0 &&
+         new_slots <= static_cast<int64_t>(pool->max_blocks_per_seq) * pool->page_size;
+}
+
 }  // namespace
 
 extern "C" {
@@ -211,6 +216,14 @@ size_t kara_workspace_bytes(kara_op op, const kara_pool* pool, int32_t num_seqs,
     case KARA_OP_LACACHE:
       if (num_seqs <= 0 || k_or_budget <= 0) return 0;
       return lacache_workspace_bytes(num_seqs, k_or_budget);
+    case KARA_OP_SPARSE:
+      if (pool == nullptr || pool->batch <= 0 || num_q_heads <= 0 || k_or_budget <= 0) return 0;
+      return sparse_workspace_bytes(pool->batch, num_q_heads, pool->num_kv_heads, pool->head_dim,
+                                    pool->max_blocks_per_seq, k_or_budget);
+    case KARA_OP_PREFIX:
+      if (pool == nullptr || pool->batch <= 0 || num_q_heads <= 0) return 0;
+      return prefix_workspace_bytes(pool->batch, num_q_heads, pool->head_dim,
+                                    pool->max_blocks_per_seq);
     default:
       return 0;
   }
@@ -489,6 +502,186 @@ kara_status lacache_compact(const kara_layer_kv* layers, int32_t num_layers,
   L.sink = params->sink;
   L.recent = params->recent;
   return launch_lacache(L, stream);
+}
+
+kara_status paged_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int32_t num_tokens,
+                              const int32_t* cu_tokens, const int32_t* positions,
+                              const float* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                              void* k_cache, void* v_cache, const kara_pool* pool,
+                              int32_t num_q_heads, void* bounds, void* q_ring, int32_t window,
+                              void* q_out, void* k_out, int32_t* dev_status,
+                              cudaStream_t stream) {
+  kara_status st = check_pool(pool);
+  if (st != KARA_OK) return st;
+  if ((st = check_heads(pool, num_q_heads)) != KARA_OK) return st;
+  if (rotary_dim < 16 || rotary_dim > pool->head_dim || rotary_dim % 16 != 0)
+    return KARA_ERR_UNSUPPORTED;
+  if (num_tokens < 0 || (cu_tokens == nullptr && num_tokens != pool->batch))
+    return KARA_ERR_INVALID_ARG;
+  if (num_tokens == 0 || pool->batch == 0) return KARA_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || positions == nullptr ||
+      inv_freq == nullptr || k_cache == nullptr || v_cache == nullptr || q_out == nullptr ||
+      dev_status == nullptr)
+    return KARA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(bounds) ||
+      !aligned16(q_ring))
+    return KARA_ERR_INVALID_ARG;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * pool->head_dim;
+  const int64_t kv_row = static_cast<int64_t>(pool->num_kv_heads) * pool->head_dim;
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 != 0 ||
+      k_stride % 8 != 0 || v_stride % 8 != 0)
+    return KARA_ERR_INVALID_ARG;
+  if (q_ring != nullptr && (window < 1 || window > KARA_MAX_WINDOW)) return KARA_ERR_INVALID_ARG;
+  RopeAppendLaunch L;
+  L.q = q;
+  L.k = k;
+  L.v = v;
+  L.q_stride = q_stride;
+  L.k_stride = k_stride;
+  L.v_stride = v_stride;
+  L.cu_tokens = cu_tokens;
+  L.positions = positions;
+  L.inv_freq = inv_freq;
+  L.k_cache = k_cache;
+  L.v_cache = v_cache;
+  L.bounds = bounds;
+  L.q_ring = q_ring;
+  L.q_out = q_out;
+  L.k_out = k_out;
+  L.block_table = pool->block_table;
+  L.ctx_len = pool->ctx_len;
+  L.status = dev_status;
+  L.T = num_tokens;
+  L.B = pool->batch;
+  L.Hq = num_q_heads;
+  L.Hkv = pool->num_kv_heads;
+  L.D = pool->head_dim;
+  L.max_blocks = pool->max_blocks_per_seq;
+  L.num_blocks = pool->num_blocks;
+  L.rotary_dim = rotary_dim;
+  L.interleaved = interleaved != 0 ? 1 : 0;
+  L.ring_w = window;
+  return launch_rope_append(L, stream);
+}
+
+kara_status paged_page_bounds(const void* k_cache, const kara_pool* pool,
+                              const int32_t* from_slot, int32_t new_slots, void* bounds,
+                              int32_t* dev_status, cudaStream_t stream) {
+  kara_status st = check_pool(pool);
+  if (st != KARA_OK) return st;
+  if (!new_slots_ok(pool, new_slots)) return KARA_ERR_INVALID_ARG;
+  if (pool->batch == 0) return KARA_OK;
+  if (k_cache == nullptr || bounds == nullptr || dev_status == nullptr || !aligned16(k_cache) ||
+      !aligned16(bounds))
+    return KARA_ERR_INVALID_ARG;
+  PageBoundsLaunch L;
+  L.k_cache = k_cache;
+  L.bounds = bounds;
+  L.block_table = pool->block_table;
+  L.ctx_len = pool->ctx_len;
+  L.from_slot = from_slot;
+  L.status = dev_status;
+  L.B = pool->batch;
+  L.Hkv = pool->num_kv_heads;
+  L.D = pool->head_dim;
+  L.max_blocks = pool->max_blocks_per_seq;
+  L.num_blocks = pool->num_blocks;
+  L.new_slots = new_slots;
+  return launch_page_bounds(L, stream);
+}
+
+kara_status paged_sparse_attn(const void* q, const void* k_cache, const void* v_cache,
+                              const void* bounds, const kara_pool* pool, int32_t num_q_heads,
+                              float scale, int32_t num_pages, int32_t sink_pages,
+                              int32_t recent_pages, int32_t new_slots, int32_t* sel, void* out,
+                              void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                              cudaStream_t stream) {
+  kara_status st = check_pool(pool);
+  if (st != KARA_OK) return st;
+  if ((st = check_heads(pool, num_q_heads)) != KARA_OK) return st;
+  if (!(scale > 0.f) || !new_slots_ok(pool, new_slots)) return KARA_ERR_INVALID_ARG;
+  if (num_pages < 1 || sink_pages < 0 || recent_pages < 1 || sink_pages > num_pages ||
+      recent_pages > num_pages - sink_pages)
+    return KARA_ERR_INVALID_ARG;
+  if (pool->batch == 0) return KARA_OK;
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || bounds == nullptr ||
+      out == nullptr || dev_status == nullptr)
+    return KARA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(bounds) ||
+      !aligned16(out))
+    return KARA_ERR_INVALID_ARG;
+  const size_t need = kara_workspace_bytes(KARA_OP_SPARSE, pool, 0, 0, num_q_heads, num_pages);
+  if (workspace == nullptr || workspace_bytes < need || !aligned256(workspace))
+    return KARA_ERR_WORKSPACE;
+  SparseLaunch L;
+  L.q = q;
+  L.k_cache = k_cache;
+  L.v_cache = v_cache;
+  L.bounds = bounds;
+  L.block_table = pool->block_table;
+  L.ctx_len = pool->ctx_len;
+  L.sel = sel;
+  L.out = out;
+  L.workspace = workspace;
+  L.status = dev_status;
+  L.B = pool->batch;
+  L.Hq = num_q_heads;
+  L.Hkv = pool->num_kv_heads;
+  L.D = pool->head_dim;
+  L.max_blocks = pool->max_blocks_per_seq;
+  L.num_blocks = pool->num_blocks;
+  L.pages = num_pages;
+  L.sink = sink_pages;
+  L.recent = recent_pages;
+  L.new_slots = new_slots;
+  L.scale = scale;
+  return launch_sparse(L, stream);
+}
+
+kara_status paged_prefix_attn(const void* q, const void* k_cache, const void* v_cache,
+                              const kara_pool* pool, int32_t num_q_heads, float scale,
+                              const int32_t* group_ptr, const int32_t* prefix_pages,
+                              int32_t num_groups, const int32_t* group_rows, int32_t new_slots,
+                              void* out, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, cudaStream_t stream) {
+  kara_status st = check_pool(pool);
+  if (st != KARA_OK) return st;
+  if ((st = check_heads(pool, num_q_heads)) != KARA_OK) return st;
+  if (num_groups < 0 || num_groups > pool->batch || !new_slots_ok(pool, new_slots))
+    return KARA_ERR_INVALID_ARG;
+  if (num_groups == 0) return KARA_OK;
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || group_ptr == nullptr ||
+      prefix_pages == nullptr || out == nullptr || dev_status == nullptr)
+    return KARA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return KARA_ERR_INVALID_ARG;
+  const size_t need = kara_workspace_bytes(KARA_OP_PREFIX, pool, 0, 0, num_q_heads, 0);
+  if (workspace == nullptr || workspace_bytes < need || !aligned256(workspace))
+    return KARA_ERR_WORKSPACE;
+  PrefixLaunch L;
+  L.q = q;
+  L.k_cache = k_cache;
+  L.v_cache = v_cache;
+  L.block_table = pool->block_table;
+  L.ctx_len = pool->ctx_len;
+  L.group_ptr = group_ptr;
+  L.group_rows = group_rows;
+  L.prefix_pages = prefix_pages;
+  L.out = out;
+  L.workspace = workspace;
+  L.status = dev_status;
+  L.B = pool->batch;
+  L.Hq = num_q_heads;
+  L.Hkv = pool->num_kv_heads;
+  L.D = pool->head_dim;
+  L.max_blocks = pool->max_blocks_per_seq;
+  L.num_blocks = pool->num_blocks;
+  L.groups = num_groups;
+  L.new_slots = new_slots;
+  L.scale = scale;
+  return launch_prefix(L, stream);
 }
 
 }  // extern "C"

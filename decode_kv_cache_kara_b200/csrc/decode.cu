@@ -32,7 +32,15 @@ namespace {
 
 constexpr int kDecThreads = 128;
 constexpr int kDecWarps = 4;
-constexpr int kUnitPages = 8;      // pages per work unit (one partial per unit)
+constexpr int kUnitPages = kDecodeUnitPages;   // pages per work unit (one partial per unit)
+
+// What the rows of a call read:
+//   kAll   every page of sequence b (the block table from page 0 on);
+//   kList  the pages named by a list per (sequence, KV head), ascending (block-sparse
+//          attention: paged_sparse_attn);
+//   kTail  for list position i the cache row rows[i].x from page rows[i].y on (what a row has
+//          behind the pages it shares: paged_prefix_attn); rows[i].x < 0 reads nothing.
+enum class Pages { kAll, kList, kTail };
 
 struct DecodeArgs {
   const __nv_bfloat16* q;
@@ -53,6 +61,11 @@ struct DecodeArgs {
   __nv_bfloat16* v_dst;
   __nv_bfloat16* q_ring;        // [B, 2W, Hq, D] or null
   int ring_w;                   // W
+  // the other page sources
+  int extra;                    // slots behind ctx_len that are read as well
+  const int32_t* sel;           // kList: [B, Hkv, sel_pages] page numbers
+  int sel_pages;
+  const int2* rows;             // kTail: (cache row, first page) per list position
 };
 
 template <int D>
@@ -80,25 +93,36 @@ __device__ __forceinline__ uint32_t sw128(int r, int gi) {
 // with consecutive unit ids (the warps of one CTA) read the KV heads of the same blocks at about
 // the same time, so each block's DRAM rows are fetched together.
 struct Unit {
-  int b, g, split, n, p0, np;   // np: pages of the unit
+  int b, g, split, n, p0, np;   // np: pages of the unit; p0: its first page (kList: list entry)
+  int row;                      // cache row (= b except for kTail)
   bool ok;
 };
 
+template <Pages SRC>
 struct UnitCursor {
   int b = 0, base = 0, per = -1, n = 0, npages = 0;
+  int2 rw = {0, 0};
   __device__ __forceinline__ Unit seek(const DecodeArgs& a, int u) {
     Unit x;
     x.ok = false;
     while (true) {
       if (b >= a.B) return x;
       if (per < 0) {
-        n = a.ctx_len[b];
+        if constexpr (SRC == Pages::kTail) {
+          // written by the kernel before the one this may run beside: not through L1
+          rw = __ldcg(a.rows + b);
+          n = rw.x < 0 ? 0 : a.ctx_len[rw.x] + a.extra;
+        } else {
+          n = a.ctx_len[b] + (SRC == Pages::kAll ? 0 : a.extra);
+        }
         if (n > a.max_blocks * 16) {
           report(a.status, KARA_ERR_INVALID_ARG);
           n = a.max_blocks * 16;
         }
         if (n < 0) n = 0;
         npages = (n + 15) / 16;
+        if constexpr (SRC == Pages::kList) npages = min(npages, a.sel_pages);
+        if constexpr (SRC == Pages::kTail) npages = max(npages - rw.y, 0);
         per = a.Hkv * ((npages + kUnitPages - 1) / kUnitPages);
       }
       if (u < base + per) break;
@@ -113,6 +137,11 @@ struct UnitCursor {
     x.n = n;
     x.p0 = x.split * kUnitPages;
     x.np = min(kUnitPages, npages - x.p0);
+    x.row = b;
+    if constexpr (SRC == Pages::kTail) {
+      x.p0 += rw.y;
+      x.row = rw.x;
+    }
     x.ok = true;
     return x;
   }
@@ -158,13 +187,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // head over the unit fixes the exponent base, so the accumulators are never rescaled. P^T goes
 // to bf16 and, transposed in registers by movmatrix, becomes the B operand of O^T (d x 8) +=
 // V^T (d x 16) P^T (16 x 8), with V^T fragments read by ldmatrix.trans.
-template <int D, int G, bool DEEP>
+template <int D, int G, bool DEEP, Pages SRC>
 __global__ void __launch_bounds__(kDecThreads, dec_min_blocks<DEEP>())
 decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a) {
   static_assert(G <= 8, "at most 8 query heads per KV head");
   constexpr int kStages = dec_stages<DEEP>();
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // previous kernel done (PDL launch)
+  // previous kernel done (PDL launch). kTail runs beside the kernel before it and reads nothing
+  // that it writes; it waits for it at its end, so that what follows sees both.
+  if constexpr (SRC != Pages::kTail) asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int NCH = D / 64;                 // 64-channel chunks per row
   constexpr int KS = D / 16;                  // k-steps of S^T, m-tiles of O^T
   constexpr uint32_t kPage = page_bytes<D>();
@@ -190,15 +221,25 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int num_warps = gridDim.x * kDecWarps;
-  UnitCursor cursor;
+  UnitCursor<SRC> cursor;
   int u = blockIdx.x * kDecWarps + warp;
   Unit cu = cursor.seek(a, u);
-  if (!cu.ok) return;
+  if (!cu.ok) {
+    if constexpr (SRC == Pages::kTail) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   Unit nu = cursor.seek(a, u + num_warps);
 
-  auto load_ids = [&](const Unit& x) -> int {
+  // kList: lane j also keeps the page number of the unit's entry j
+  auto load_pages = [&](const Unit& x) -> int {
+    if (SRC != Pages::kList || !x.ok || lane >= x.np) return 0;
+    const int p = a.sel[(static_cast<size_t>(x.b) * a.Hkv + x.g) * a.sel_pages + x.p0 + lane];
+    return min(max(p, 0), a.max_blocks - 1);
+  };
+  auto load_ids = [&](const Unit& x, int page) -> int {
     if (!x.ok || lane >= x.np) return -1;
-    int blk = a.block_table[static_cast<size_t>(x.b) * a.max_blocks + x.p0 + lane];
+    int blk = a.block_table[static_cast<size_t>(x.row) * a.max_blocks +
+                            (SRC == Pages::kList ? page : x.p0 + lane)];
     if (blk < 0 || blk >= a.num_blocks) {
       report(a.status, KARA_ERR_BAD_BLOCK);
       blk = -1;
@@ -210,7 +251,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
   auto load_q = [&](const Unit& x, uint32_t (&qb)[KS][2]) {
     const bool row_ok = x.ok && grp < G;
     const uint32_t* qrow = reinterpret_cast<const uint32_t*>(
-        a.q + (static_cast<size_t>(x.b) * a.Hq + x.g * G + (row_ok ? grp : 0)) * D);
+        a.q + (static_cast<size_t>(x.ok ? x.row : 0) * a.Hq + x.g * G + (row_ok ? grp : 0)) * D);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       qb[ks][0] = row_ok ? qrow[ks * 8 + tig] : 0u;
@@ -218,7 +259,15 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
   };
 
-  int ids_cu = load_ids(cu), ids_nu = load_ids(nu);
+  int pages_cu = load_pages(cu), pages_nu = load_pages(nu);
+  int ids_cu = load_ids(cu, pages_cu), ids_nu = load_ids(nu, pages_nu);
+  // slots of the unit's page j that the sequence holds (16 except in its last page)
+  auto valid_slots = [&](int j) -> int {
+    if constexpr (SRC == Pages::kList)
+      return min(16, cu.n - __shfl_sync(0xffffffffu, pages_cu, j) * 16);
+    else
+      return min(16, cu.n - (cu.p0 + j) * 16);
+  };
   uint32_t qb[KS][2], qn[KS][2];
   load_q(cu, qb);
   load_q(nu, qn);
@@ -292,7 +341,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[0][e] += acc[1][e];
           // acc: (slot grp, heads 2tig, 2tig+1), (slot grp+8, heads 2tig, 2tig+1)
-          const int valid = min(16, cu.n - (cu.p0 + j) * 16);
+          const int valid = valid_slots(j);
           const bool lo_ok = grp < valid, hi_ok = grp + 8 < valid;
           sc[j][0] = lo_ok ? acc[0][0] * a.cs : -INFINITY;
           sc[j][1] = lo_ok ? acc[0][1] * a.cs : -INFINITY;
@@ -338,7 +387,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int blk = __shfl_sync(0xffffffffu, ids_cu, j);
         const uint32_t vst = acquire(ustart + cu.np + j, blk);
         if (vst != 0u) {
-          const int valid = min(16, cu.n - (cu.p0 + j) * 16);
+          const int valid = valid_slots(j);
           // slots past the context may hold any bits (even NaN); P is 0 there, V is zeroed
           const int s_lo = 2 * tig, s_hi = 8 + 2 * tig;
           const uint32_t mlo = (s_lo < valid ? 0xffffu : 0u) | (s_lo + 1 < valid ? 0xffff0000u : 0u);
@@ -388,6 +437,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
     ustart += 2 * cu.np;
     cu = nu;
     ids_cu = ids_nu;
+    pages_cu = pages_nu;
     if (!cu.ok) break;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -396,7 +446,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     u += num_warps;
     nu = cursor.seek(a, u + num_warps);
-    ids_nu = load_ids(nu);
+    pages_nu = load_pages(nu);
+    ids_nu = load_ids(nu, pages_nu);
     load_q(nu, qn);
   }
   if (aborted) {
@@ -405,6 +456,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
     for (int st = 0; st < kStages; ++st)
       if ((pending >> st) & 1u) mbar_wait(&my_bars[st], (phase >> st) & 1, &give_up, a.status);
   }
+  if constexpr (SRC == Pages::kTail) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Merge of the split partials of each (sequence, query head): one CTA of kCombWarps warps per
@@ -432,9 +484,11 @@ decode_combine_kernel(const DecodeArgs a, __nv_bfloat16* __restrict__ out) {
   const int bh = blockIdx.x;
   const int warp = warp_id(), lane = lane_id();
   const int b = bh / a.Hq;
-  int n = a.ctx_len[b];
+  int n = a.ctx_len[b] + a.extra;
   n = max(0, min(n, a.max_blocks * 16));
-  const int splits = (((n + 15) / 16) + kUnitPages - 1) / kUnitPages;
+  int npages = (n + 15) / 16;
+  if (a.sel != nullptr) npages = min(npages, a.sel_pages);
+  const int splits = (npages + kUnitPages - 1) / kUnitPages;
   const float2* ml = a.part_ml + static_cast<size_t>(bh) * a.S;
   const float* po = a.part_o + static_cast<size_t>(bh) * a.S * D + lane * V;
   float mx = -INFINITY;
@@ -544,7 +598,7 @@ decode_combine_kernel(const DecodeArgs a, __nv_bfloat16* __restrict__ out) {
   }
 }
 
-template <int D, int G, bool DEEP>
+template <int D, int G, bool DEEP, Pages SRC>
 kara_status launch_dg(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, void* out,
                       cudaStream_t stream) {
   constexpr size_t smem = stream_smem_bytes<D, DEEP>();
@@ -555,16 +609,17 @@ kara_status launch_dg(const DecodeArgs& a, const CUtensorMap& tk, const CUtensor
     return KARA_ERR_CUDA;
   }
   if (per_sm[dev].load() == 0) {
-    cudaFuncSetAttribute(decode_stream_kernel<D, G, DEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(decode_stream_kernel<D, G, DEEP, SRC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          static_cast<int>(smem));
     int n = 0;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_stream_kernel<D, G, DEEP>, kDecThreads, smem);
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_stream_kernel<D, G, DEEP, SRC>, kDecThreads, smem);
     per_sm[dev].store(n > 0 ? n : 1);
   }
   int sms = 148;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  launch_pdl(decode_stream_kernel<D, G, DEEP>, dim3(per_sm[dev].load() * sms), dim3(kDecThreads), smem,
+  launch_pdl(decode_stream_kernel<D, G, DEEP, SRC>, dim3(per_sm[dev].load() * sms), dim3(kDecThreads), smem,
              stream, tk, tv, a);
+  if (SRC == Pages::kTail) return check_launch("paged_prefix_attn");   // its caller combines
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.B * a.Hq);
   cfg.blockDim = dim3(32 * kCombWarps);
@@ -587,25 +642,25 @@ kara_status launch_dg(const DecodeArgs& a, const CUtensorMap& tk, const CUtensor
 template <int D, int G>
 constexpr bool deep_ring() { return D == 128 && G <= 6; }
 
-template <int D>
+template <int D, Pages SRC>
 kara_status launch_d(const DecodeArgs& a, int G, const CUtensorMap& tk, const CUtensorMap& tv,
                      void* out, cudaStream_t stream) {
   switch (G) {
-    case 1: return launch_dg<D, 1, deep_ring<D, 1>()>(a, tk, tv, out, stream);
-    case 2: return launch_dg<D, 2, deep_ring<D, 2>()>(a, tk, tv, out, stream);
-    case 3: return launch_dg<D, 3, deep_ring<D, 3>()>(a, tk, tv, out, stream);
-    case 4: return launch_dg<D, 4, deep_ring<D, 4>()>(a, tk, tv, out, stream);
-    case 5: return launch_dg<D, 5, deep_ring<D, 5>()>(a, tk, tv, out, stream);
-    case 6: return launch_dg<D, 6, deep_ring<D, 6>()>(a, tk, tv, out, stream);
-    case 7: return launch_dg<D, 7, deep_ring<D, 7>()>(a, tk, tv, out, stream);
-    case 8: return launch_dg<D, 8, deep_ring<D, 8>()>(a, tk, tv, out, stream);
+    case 1: return launch_dg<D, 1, deep_ring<D, 1>(), SRC>(a, tk, tv, out, stream);
+    case 2: return launch_dg<D, 2, deep_ring<D, 2>(), SRC>(a, tk, tv, out, stream);
+    case 3: return launch_dg<D, 3, deep_ring<D, 3>(), SRC>(a, tk, tv, out, stream);
+    case 4: return launch_dg<D, 4, deep_ring<D, 4>(), SRC>(a, tk, tv, out, stream);
+    case 5: return launch_dg<D, 5, deep_ring<D, 5>(), SRC>(a, tk, tv, out, stream);
+    case 6: return launch_dg<D, 6, deep_ring<D, 6>(), SRC>(a, tk, tv, out, stream);
+    case 7: return launch_dg<D, 7, deep_ring<D, 7>(), SRC>(a, tk, tv, out, stream);
+    case 8: return launch_dg<D, 8, deep_ring<D, 8>(), SRC>(a, tk, tv, out, stream);
     default: return KARA_ERR_UNSUPPORTED;
   }
 }
 
 }  // namespace
 
-int decode_num_splits(int max_blocks) { return (max_blocks + kUnitPages - 1) / kUnitPages; }
+int decode_num_splits(int pages) { return (pages + kUnitPages - 1) / kUnitPages; }
 
 size_t decode_workspace_bytes(int B, int Hq, int D, int max_blocks) {
   return static_cast<size_t>(B) * Hq * decode_num_splits(max_blocks) * (D + 2) * sizeof(float);
@@ -620,7 +675,7 @@ kara_status launch_decode(const DecodeLaunch& L, cudaStream_t stream) {
   a.block_table = L.block_table;
   a.ctx_len = L.ctx_len;
   // workspace: o rows [B, Hq, S, D] first, then (m, l) pairs [B, Hq, S]
-  a.S = decode_num_splits(L.max_blocks);
+  a.S = decode_num_splits(L.sel != nullptr ? L.sel_pages : L.max_blocks);
   a.part_o = L.partial;
   a.part_ml = reinterpret_cast<float2*>(L.partial + static_cast<size_t>(L.B) * L.Hq * a.S * L.D);
   a.status = L.status;
@@ -637,6 +692,10 @@ kara_status launch_decode(const DecodeLaunch& L, cudaStream_t stream) {
   a.v_dst = static_cast<__nv_bfloat16*>(const_cast<void*>(L.v_cache));
   a.q_ring = static_cast<__nv_bfloat16*>(L.q_ring);
   a.ring_w = L.ring_w;
+  a.extra = L.extra;
+  a.sel = L.sel;
+  a.sel_pages = L.sel_pages;
+  a.rows = L.rows;
   const int G = L.Hq / L.Hkv;
   // paged pools as 4-D maps {d, Hkv, 16 slots, blocks}; box = one page of one KV head, 64
   // channels wide, 128-byte swizzle (the same map shape the scoring kernels use)
@@ -648,9 +707,16 @@ kara_status launch_decode(const DecodeLaunch& L, cudaStream_t stream) {
   if (!make_bf16_map_4d(&tk, L.k_cache, dims, strides, 16) ||
       !make_bf16_map_4d(&tv, L.v_cache, dims, strides, 16))
     return KARA_ERR_CUDA;
-  if (L.D == 128) return launch_d<128>(a, G, tk, tv, L.out, stream);
-  if (L.D == 64) return launch_d<64>(a, G, tk, tv, L.out, stream);
-  return KARA_ERR_UNSUPPORTED;
+  if (L.D != 128 && L.D != 64) return KARA_ERR_UNSUPPORTED;
+  const bool wide = L.D == 128;
+  if (L.rows != nullptr)
+    return wide ? launch_d<128, Pages::kTail>(a, G, tk, tv, L.out, stream)
+                : launch_d<64, Pages::kTail>(a, G, tk, tv, L.out, stream);
+  if (L.sel != nullptr)
+    return wide ? launch_d<128, Pages::kList>(a, G, tk, tv, L.out, stream)
+                : launch_d<64, Pages::kList>(a, G, tk, tv, L.out, stream);
+  return wide ? launch_d<128, Pages::kAll>(a, G, tk, tv, L.out, stream)
+              : launch_d<64, Pages::kAll>(a, G, tk, tv, L.out, stream);
 }
 
 }  // namespace kara

@@ -148,10 +148,90 @@ struct DecodeLaunch {
   const void* v_new = nullptr;
   void* q_ring = nullptr;
   int ring_w = 0;
+  // other page sources (at most one of sel and rows): the pages of a list per (sequence, KV
+  // head), or for every list position a cache row and its first page; in the latter case B
+  // counts list positions, only the partials are computed, and the kernel runs beside the one
+  // launched before it (which must not write `rows` and must have waited for its writer)
+  int extra = 0;                   // slots behind ctx_len that are read as well
+  const int32_t* sel = nullptr;    // [B, Hkv, sel_pages]
+  int sel_pages = 0;
+  const int2* rows = nullptr;      // [B] (cache row or -1, first page)
 };
-int decode_num_splits(int max_blocks);
+// Pages per work unit of the streaming decode kernel: one partial (m, l, o) per unit.
+constexpr int kDecodeUnitPages = 8;
+int decode_num_splits(int pages);
 size_t decode_workspace_bytes(int B, int Hq, int D, int max_blocks);
 kara_status launch_decode(const DecodeLaunch& L, cudaStream_t stream);
+
+struct RopeAppendLaunch {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;   // elements between tokens
+  const int32_t* cu_tokens;
+  const int32_t* positions;
+  const float* inv_freq;
+  void* k_cache;
+  void* v_cache;
+  void* bounds;
+  void* q_ring;
+  void* q_out;
+  void* k_out;
+  const int32_t* block_table;
+  const int32_t* ctx_len;
+  int32_t* status;
+  int T, B, Hq, Hkv, D, max_blocks, num_blocks, rotary_dim, interleaved, ring_w;
+};
+kara_status launch_rope_append(const RopeAppendLaunch& L, cudaStream_t stream);
+
+struct PageBoundsLaunch {
+  const void* k_cache;
+  void* bounds;
+  const int32_t* block_table;
+  const int32_t* ctx_len;
+  const int32_t* from_slot;
+  int32_t* status;
+  int B, Hkv, D, max_blocks, num_blocks, new_slots;
+};
+kara_status launch_page_bounds(const PageBoundsLaunch& L, cudaStream_t stream);
+
+struct SparseLaunch {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const void* bounds;
+  const int32_t* block_table;
+  const int32_t* ctx_len;
+  int32_t* sel;      // [B, Hkv, pages] (the caller's or the workspace's)
+  void* out;
+  void* workspace;
+  int32_t* status;
+  int B, Hq, Hkv, D, max_blocks, num_blocks;
+  int pages, sink, recent, new_slots;
+  float scale;
+};
+size_t sparse_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks, int pages);
+kara_status launch_sparse(const SparseLaunch& L, cudaStream_t stream);
+
+struct PrefixLaunch {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_table;
+  const int32_t* ctx_len;
+  const int32_t* group_ptr;
+  const int32_t* group_rows;
+  const int32_t* prefix_pages;
+  void* out;
+  void* workspace;
+  int32_t* status;
+  int B, Hq, Hkv, D, max_blocks, num_blocks;
+  int groups, new_slots;
+  float scale;
+};
+size_t prefix_workspace_bytes(int B, int Hq, int D, int max_blocks);
+kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream);
+
 kara_status launch_step_begin(const kara_pool* pool, int32_t* dev_status, cudaStream_t stream);
 kara_status launch_step_end(const kara_pool* pool, int32_t* tail, int32_t window,
                             int32_t capacity, int32_t check, int32_t* due, int32_t* due_count,

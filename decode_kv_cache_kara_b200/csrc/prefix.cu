@@ -1,0 +1,753 @@
+// Decode attention of rows that share their first pages (paged_prefix_attn): N sequences
+// behind one prompt, or many samples of it, read the shared K and V once for all.
+//
+// For a group of N rows with a prefix of P pages, the N * G queries of a KV head form one
+// matrix: S = Q K^T and O += P V on tcgen05 with 128 keys per step, so a byte of the prefix
+// serves N * G queries instead of G. Every row's own slots behind the prefix go through the
+// streaming decode kernel. Softmax statistics are base 2 and partial results (m, l, o), which
+// join at the end:
+//     m = max m_i,  l = sum 2^(m_i - m) l_i,  out = sum 2^(m_i - m) o_i / l.
+// Four kernels: plan (groups, rows, the prefix work in units of 128 keys), prefix, tail (the
+// streaming kernel, beside the prefix kernel), combine.
+//
+// The prefix work of all groups, tiles of 256 queries and KV heads is one line of key tiles,
+// cut into equal parts, one per block: all blocks finish together whatever the groups' sizes,
+// and an item (group, query tile, KV head) that spans several parts leaves one partial in each.
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+#include "row_items.cuh"
+
+namespace kara {
+
+namespace {
+
+constexpr int kKeys = 128;              // keys per step
+constexpr int kTilePages = kKeys / 16;
+constexpr int kRows = 128;              // query rows per tensor-core tile
+constexpr int kItemRows = 2 * kRows;    // query rows per item: one tile per softmax team
+constexpr int kMaxCtas = 160;           // grid limit (workspace rows are sized by it)
+constexpr int kMinTiles = 2;            // key tiles that are worth a block of their own
+
+// Written by the plan kernel.
+struct PlanHead {
+  long long total;     // key tiles of all items
+  int ctas;            // blocks with prefix work
+  int pad;
+};
+struct PlanGroup {
+  long long flat;      // key tiles of the groups before
+  int first, rows;     // list positions [first, first + rows)
+  int ktiles;          // key tiles per item (0: no shared part)
+  int pages;           // prefix pages
+  int row0;            // cache row whose table names the prefix pages
+  int pad;
+};
+
+struct PrefixArgs {
+  const __nv_bfloat16* q;
+  const int32_t* block_table;
+  const int32_t* ctx_len;
+  const int32_t* group_ptr;
+  const int32_t* group_rows;     // or null: list position = cache row
+  const int32_t* prefix_pages;
+  PlanHead* head;
+  PlanGroup* groups;
+  int2* rows;                    // [B]: (cache row or -1, first own page)
+  int* row_group;                // [B]
+  float* part_o;                 // prefix partials: [Hq B + 256 ctas, D]
+  float2* part_ml;
+  const float* tail_o;           // the streaming kernel's: [B, Hq, S, D]
+  const float2* tail_ml;
+  __nv_bfloat16* out;
+  int32_t* status;
+  int B, Hq, Hkv, G, max_blocks, num_blocks, num_groups, extra, S, ctas;
+  float cs;                      // |scale| * log2(e)
+  int negate;                    // scale < 0: the queries' signs are flipped
+};
+
+constexpr int kPlanThreads = 256;
+
+// One block. A group of one row has nothing to share: its pages are all its own.
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ RowItems<kPlanThreads> items;
+  long long flat = 0;
+  for (int j0 = 0; j0 < a.num_groups; j0 += kPlanThreads) {
+    const int j = j0 + static_cast<int>(threadIdx.x);
+    PlanGroup gr = {};
+    int len = 0;
+    if (j < a.num_groups) {
+      const int lo = a.group_ptr[j], hi = a.group_ptr[j + 1], pages = a.prefix_pages[j];
+      if (lo < 0 || hi < lo || hi > a.B || pages < 0 || pages > a.max_blocks) {
+        report(a.status, KARA_ERR_INVALID_ARG);
+      } else if (hi > lo) {
+        gr.first = lo;
+        gr.rows = hi - lo;
+        gr.pages = pages;
+        gr.row0 = a.group_rows != nullptr ? a.group_rows[lo] : lo;
+        if (gr.row0 < 0 || gr.row0 >= a.B) {
+          report(a.status, KARA_ERR_INVALID_ARG);
+          gr.rows = 0;
+        } else if (gr.rows > 1) {
+          gr.ktiles = (pages + kTilePages - 1) / kTilePages;
+          len = (gr.rows * a.G + kItemRows - 1) / kItemRows * a.Hkv * gr.ktiles;
+        }
+      }
+    }
+    row_items_scan(items, len);
+    if (j < a.num_groups) {
+      gr.flat = flat + items.start[threadIdx.x];
+      a.groups[j] = gr;
+    }
+    flat += items.start[kPlanThreads];
+  }
+  if (threadIdx.x == 0) {
+    const long long most = flat / kMinTiles;
+    a.head->total = flat;
+    a.head->ctas = static_cast<int>(most < 1 ? 1 : most < a.ctas ? most : a.ctas);
+  }
+  __syncthreads();               // the groups are written
+  for (int i = threadIdx.x; i < a.B; i += kPlanThreads) {
+    int2 r = make_int2(-1, 0);
+    int lo = 0, hi = a.num_groups;               // ptr[lo] <= i < ptr[hi] where there is one
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.group_ptr[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    const PlanGroup gr = a.groups[lo];
+    if (i >= gr.first && i < gr.first + gr.rows) {
+      const int row = a.group_rows != nullptr ? a.group_rows[i] : i;
+      if (row < 0 || row >= a.B) {
+        report(a.status, KARA_ERR_INVALID_ARG);
+      } else {
+        const int n = a.ctx_len[row];
+        const long long len = static_cast<long long>(n) + a.extra;
+        if (n < 0 || len < static_cast<long long>(gr.pages) * 16 ||
+            len > static_cast<long long>(a.max_blocks) * 16)
+          report(a.status, KARA_ERR_INVALID_ARG);
+        r = make_int2(row, gr.rows > 1 ? gr.pages : 0);
+      }
+    }
+    a.rows[i] = r;
+    a.row_group[i] = lo;
+  }
+}
+
+// The part of an item that one block works on: key tiles [kt0, kt1).
+struct Seg {
+  int first, row0, pages, g, kt0, kt1, q0, rows;   // q0: first query row of the item in its group
+  long long out_row;                               // first partial row
+};
+
+// Walks block c's part of the line of key tiles.
+struct SegCursor {
+  long long pos, end;
+  int c, j;
+  __device__ __forceinline__ void init(const PrefixArgs& a, int cta) {
+    c = cta;
+    const long long total = a.head->total;
+    const int n = a.head->ctas;
+    pos = end = 0;
+    j = 0;
+    if (cta >= n) return;
+    pos = total * cta / n;
+    end = total * (cta + 1) / n;
+    int lo = 0, hi = a.num_groups;               // the last group with flat <= pos
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.groups[mid].flat <= pos) lo = mid;
+      else hi = mid;
+    }
+    j = lo;
+  }
+  __device__ __forceinline__ bool next(const PrefixArgs& a, Seg& s) {
+    if (pos >= end) return false;
+    PlanGroup gr = a.groups[j];
+    while (j + 1 < a.num_groups && a.groups[j + 1].flat <= pos) gr = a.groups[++j];
+    const int local = static_cast<int>(pos - gr.flat);
+    const int x = local / gr.ktiles;
+    const int t = x / a.Hkv;
+    s.g = x - t * a.Hkv;
+    s.kt0 = local - x * gr.ktiles;
+    s.kt1 = static_cast<int>(min(static_cast<long long>(gr.ktiles), s.kt0 + (end - pos)));
+    s.first = gr.first;
+    s.row0 = gr.row0;
+    s.pages = gr.pages;
+    s.q0 = t * kItemRows;
+    s.rows = min(kItemRows, gr.rows * a.G - s.q0);
+    s.out_row = static_cast<long long>(a.Hq) * gr.first + static_cast<long long>(s.q0) * a.Hkv +
+                static_cast<long long>(s.g) * s.rows + static_cast<long long>(kItemRows) * c;
+    pos += s.kt1 - s.kt0;
+    return true;
+  }
+};
+
+constexpr int kPfxThreads = 384;        // warp 0: TMA, warp 1: UMMA, warps 4-11: softmax teams
+constexpr uint32_t kTmemS = 0;          // S of team w at 128 w; its P (bf16) over S's columns
+constexpr uint32_t kTmemO = 256;        // O of team w at 256 + 128 w
+
+template <int D>
+struct PfxSmem {
+  static constexpr int NCH = D / 64;
+  static constexpr uint32_t kChunk = kKeys * 128;          // 64 channels of 128 rows
+  static constexpr uint32_t kTile = NCH * kChunk;          // one K or V tile, one Q tile
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr uint32_t q_off = 0;
+  static constexpr uint32_t kv_off = 2 * kTile;
+  static constexpr uint32_t bar_off = kv_off + kStages * kTile;
+  static constexpr int kBars = 2 * kStages + 2 * 4 + 1;
+  static constexpr uint32_t bytes = bar_off + kBars * 8 + 16;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPfxThreads, 1)
+prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const PrefixArgs a) {
+  using L = PfxSmem<D>;
+  constexpr int NCH = L::NCH;
+  constexpr int kStages = L::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* q_buf = smem + L::q_off;
+  uint8_t* kv_buf = smem + L::kv_off;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
+  uint64_t* kv_empty = kv_full + kStages;
+  uint64_t* q_full = kv_empty + kStages;      // [2] the team's queries are in shared memory
+  uint64_t* s_full = q_full + 2;              // [2]
+  uint64_t* p_full = s_full + 2;              // [2] P written, S read, O rescaled
+  uint64_t* o_full = p_full + 2;              // [2] the segment's products are done
+  uint64_t* drained = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = warp_id(), lane = lane_id();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&q_full[w], 4);
+      mbar_init(&s_full[w], 1);
+      mbar_init(&p_full[w], 4);
+      mbar_init(&o_full[w], 1);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan is written
+  // the streaming kernel may start: it reads the plan only, and waits for this kernel at its end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  SegCursor cur;
+  cur.init(a, blockIdx.x);
+  Seg sg;
+
+  if (warp == 0) {
+    // ---- TMA producer: K(0), then K(i), V(i - 1), the order of use ----
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    int issued = 0;
+    bool ok = true;
+    const int page = lane / NCH, ch = lane % NCH;
+    while (ok && cur.next(a, sg)) {
+      const int32_t* table = a.block_table + static_cast<size_t>(sg.row0) * a.max_blocks;
+      // pages past the prefix in its last tile: its last page again (their weights are 0)
+      auto block_of = [&](int kt) -> int {
+        if (lane >= kTilePages * NCH) return 0;
+        int blk = table[min(kt * kTilePages + page, sg.pages - 1)];
+        if (blk < 0 || blk >= a.num_blocks) {
+          report(a.status, KARA_ERR_BAD_BLOCK);
+          blk = 0;
+        }
+        return blk;
+      };
+      auto load = [&](const CUtensorMap* tm, int blk) -> bool {
+        const int st = issued % kStages;
+        int go = 1;
+        if (lane == 0) {
+          go = mbar_wait(&kv_empty[st], ((issued / kStages) & 1) ^ 1, abort_flag, a.status) ? 1 : 0;
+          if (go) mbar_expect_tx(&kv_full[st], L::kTile);
+        }
+        if (!__shfl_sync(0xffffffffu, go, 0)) return false;
+        if (lane < kTilePages * NCH)
+          tma_load_4d(kv_buf + st * L::kTile + ch * L::kChunk + page * 2048, tm, &kv_full[st],
+                      ch * 64, sg.g, 0, blk);
+        ++issued;
+        return true;
+      };
+      int blk = block_of(sg.kt0), blk_v = 0;
+      for (int kt = sg.kt0; ok && kt <= sg.kt1; ++kt) {
+        const int blk_next = kt + 1 < sg.kt1 ? block_of(kt + 1) : 0;
+        if (kt < sg.kt1) ok = load(&tm_k, blk);
+        if (ok && kt > sg.kt0) ok = load(&tm_v, blk_v);
+        blk_v = blk;
+        blk = blk_next;
+      }
+    }
+    if (!ok) {
+      // a wait gave up (reported): let the copies in flight land before the block leaves
+      volatile int give_up = 0;
+      for (int st = 0; st < kStages; ++st)
+        if (issued > st)
+          mbar_wait(&kv_full[st], ((issued - 1 - st) / kStages) & 1, &give_up, a.status);
+    }
+  } else if (warp == 1) {
+    // ---- UMMA issuer. Per step i and team w: O_w += P_w(i-1) V(i-1), then S_w(i) = Q_w K(i)^T,
+    // so that one team's products run while the other team exponentiates. S_w(i) overwrites
+    // P_w(i-1) in tensor memory: products execute in issue order. ----
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D) | (1u << 16);   // V is N-major
+      uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+      int used = 0;                             // ring entries consumed
+      bool ok = true;
+      while (ok && cur.next(a, sg)) {
+        const int teams = sg.rows > kRows ? 2 : 1;
+        const int n = sg.kt1 - sg.kt0;
+        for (int w = 0; ok && w < teams; ++w) {
+          ok = mbar_wait(&q_full[w], q_ph[w], abort_flag, a.status);
+          q_ph[w] ^= 1;
+        }
+        for (int i = 0; ok && i <= n; ++i) {
+          const int k_at = used, v_at = used + (i < n ? 1 : 0);
+          const int ks = k_at % kStages, vs = v_at % kStages;
+          if (i < n) ok = mbar_wait(&kv_full[ks], (k_at / kStages) & 1, abort_flag, a.status);
+          if (ok && i > 0)
+            ok = mbar_wait(&kv_full[vs], (v_at / kStages) & 1, abort_flag, a.status);
+          for (int w = 0; ok && w < teams; ++w) {
+            if (i > 0) {
+              ok = mbar_wait(&p_full[w], p_ph[w], abort_flag, a.status);
+              if (!ok) break;
+              p_ph[w] ^= 1;
+              tc_fence_after();
+              const uint32_t v_addr = smem_u32(kv_buf + vs * L::kTile);
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                umma_bf16_ts(tmem + kTmemO + w * 128, tmem + kTmemS + w * 128 + k * 8,
+                             sw128_mnmajor_desc(v_addr + k * 2048, L::kChunk, 1024), idesc_o,
+                             (i > 1 || k > 0) ? 1u : 0u);
+              if (i == n) umma_commit(&o_full[w]);
+            }
+            if (i < n) {
+              tc_fence_after();
+              const uint32_t q_addr = smem_u32(q_buf + w * L::kTile);
+              const uint32_t k_addr = smem_u32(kv_buf + ks * L::kTile);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * L::kChunk + (k & 3) * 32;
+                umma_bf16(tmem + kTmemS + w * 128, sw128_kmajor_desc(q_addr + off),
+                          sw128_kmajor_desc(k_addr + off), idesc_s, k > 0 ? 1u : 0u);
+              }
+              umma_commit(&s_full[w]);
+            }
+          }
+          if (ok && i > 0) umma_commit(&kv_empty[vs]);
+          if (ok && i < n) umma_commit(&kv_empty[ks]);
+          used += (i < n ? 1 : 0) + (i > 0 ? 1 : 0);
+        }
+      }
+      if (!ok) {                                // products in flight still read shared memory
+        volatile int give_up = 0;
+        umma_commit(drained);
+        mbar_wait(drained, 0, &give_up, a.status);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---- softmax teams: a thread owns one query row (TMEM lane) ----
+    const int w = (warp - 4) >> 2;
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t s_col = lane_base + kTmemS + w * 128;
+    const uint32_t o_col = lane_base + kTmemO + w * 128;
+    uint8_t* q_tile = q_buf + w * L::kTile;
+    const uint32_t flip = a.negate ? 0x80008000u : 0u;
+    uint32_t s_ph = 0, o_ph = 0;
+    bool aborted = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool ok = aborted ? false : mbar_wait(bar, parity, abort_flag, a.status);
+      aborted = __any_sync(0xffffffffu, !ok) != 0;
+    };
+    while (!aborted && cur.next(a, sg)) {
+      const int live = sg.rows - w * kRows;     // rows of this team that exist
+      if (live <= 0) continue;
+      const bool warp_on = quad * 32 < live;
+      // the warp's 32 query rows into the swizzled tile, 16 bytes per lane, whole rows at a time
+      if (warp_on) {
+        constexpr int kPer = D / 8;             // lanes per row
+        for (int r0 = 0; r0 < 32; r0 += 32 / kPer) {
+          const int r = quad * 32 + r0 + lane / kPer, gi = lane % kPer;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (r < live) {
+            const int qr = sg.q0 + w * kRows + r;
+            const int member = qr / a.G, h = qr - member * a.G;
+            const int i = sg.first + member;
+            int b = a.group_rows != nullptr ? a.group_rows[i] : i;
+            b = min(max(b, 0), a.B - 1);        // a bad row is reported by the plan
+            x = *reinterpret_cast<const uint4*>(
+                a.q + (static_cast<size_t>(b) * a.Hq + sg.g * a.G + h) * D + gi * 8);
+            x.x ^= flip;
+            x.y ^= flip;
+            x.z ^= flip;
+            x.w ^= flip;
+          }
+          *reinterpret_cast<uint4*>(q_tile + (gi >> 3) * L::kChunk + (r >> 3) * 1024 +
+                                    (r & 7) * 128 + (((gi & 7) ^ (r & 7)) << 4)) = x;
+        }
+        fence_proxy_async();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[w]);
+      float m = -INFINITY, l = 0.f;             // m: the exponent base, in units of raw S
+      const int n = sg.kt1 - sg.kt0;
+      for (int i = 0; i < n; ++i) {
+        wait(&s_full[w], s_ph);
+        s_ph ^= 1;
+        if (aborted) break;
+        if (warp_on) {
+          tc_fence_after();
+          const int valid = min(kKeys, (sg.pages - (sg.kt0 + i) * kTilePages) * 16);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) {
+            float v[32];
+            tmem_ld32(s_col + c, v);
+            tmem_wait_ld();
+            reg_fence<32>(v);
+            if (valid < kKeys) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = c + e < valid ? v[e] : -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) mx = fmax3(mx, v[e], v[e + 1]);
+          }
+          // the base moves only when the row maximum outgrows it by 2^8 (or on the first tile):
+          // weights up to 2^8 lose nothing in fp32 sums and floating bf16
+          const bool move = i == 0 || (mx - m) * a.cs > 8.f;
+          if (i == 0) {
+            m = mx;
+          } else if (__any_sync(0xffffffffu, move)) {
+            // P V(i - 1) is complete: it was issued before S(i)
+            const float to = move ? mx : m;
+            const float f = ex2((m - to) * a.cs);
+            m = to;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float v[16];
+              uint32_t u[16];
+              tmem_ld16(o_col + c, v);
+              tmem_wait_ld();
+              reg_fence<16>(v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * f);
+              tmem_st16(o_col + c, u);
+            }
+          }
+          const float nb = m == -INFINITY ? 0.f : -m * a.cs;
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) {
+            float v[32];
+            uint32_t u[16];
+            tmem_ld32(s_col + c, v);
+            tmem_wait_ld();
+            reg_fence<32>(v);
+            if (valid < kKeys) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = c + e < valid ? v[e] : -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = ffma2(make_float2(v[e], v[e + 1]), make_float2(a.cs, a.cs),
+                                     make_float2(nb, nb));
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
+              sum = fadd2(sum, p);
+              const __nv_bfloat162 pb = __floats2bfloat162_rn(p.x, p.y);
+              u[e / 2] = *reinterpret_cast<const uint32_t*>(&pb);
+            }
+            tmem_st16(s_col + c / 2, u);
+          }
+          l += sum.x + sum.y;
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
+      }
+      if (aborted) break;
+      wait(&o_full[w], o_ph);
+      o_ph ^= 1;
+      if (aborted) break;
+      if (warp_on) {
+        tc_fence_after();
+        const size_t r = static_cast<size_t>(sg.out_row) + w * kRows + row;
+        if (row < live) a.part_ml[r] = make_float2(m * a.cs, l);
+        float* dst = a.part_o + r * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld32(o_col + c, v);
+          tmem_wait_ld();
+          reg_fence<32>(v);
+          if (row < live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(dst + c + e) =
+                  make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          }
+        }
+        tc_fence_before();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// One block per (list position, query head): the partials of the row's share of the prefix
+// (one per block that worked on its item) and of its own slots (one per 8 pages). Warps take
+// partials in turn, a lane owns D / 32 channels.
+constexpr int kJoinWarps = 4;
+constexpr int kJoinBatch = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) prefix_combine_kernel(const PrefixArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int V = D / 32;
+  __shared__ float red_o[kJoinWarps][D];
+  __shared__ float red_l[kJoinWarps];
+  const int i = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
+  const int warp = warp_id(), lane = lane_id();
+  const int2 rw = a.rows[i];
+  if (rw.x < 0) return;                          // not in a group: its output stays as it was
+  int n = a.ctx_len[rw.x] + a.extra;
+  n = max(0, min(n, a.max_blocks * 16));
+  const int own = max((n + 15) / 16 - rw.y, 0);
+  const int splits = (own + kDecodeUnitPages - 1) / kDecodeUnitPages;
+  // the row's item and the blocks [c0, c0 + npre) that share it
+  const PlanGroup gr = a.groups[a.row_group[i]];
+  int c0 = 0, npre = 0;
+  long long row = 0;
+  if (gr.ktiles > 0) {
+    const int g = h / a.G;
+    const int qr = (i - gr.first) * a.G + h - g * a.G;
+    const int t = qr / kItemRows, r = qr - t * kItemRows;
+    const int rows_t = min(kItemRows, gr.rows * a.G - t * kItemRows);
+    const long long a0 = gr.flat + static_cast<long long>(t * a.Hkv + g) * gr.ktiles;
+    const long long total = a.head->total;
+    const int ctas = a.head->ctas;
+    c0 = static_cast<int>(((a0 + 1) * ctas - 1) / total);
+    npre = static_cast<int>(((a0 + gr.ktiles) * ctas - 1) / total) - c0 + 1;
+    row = static_cast<long long>(a.Hq) * gr.first + static_cast<long long>(t) * kItemRows * a.Hkv +
+          static_cast<long long>(g) * rows_t + r + static_cast<long long>(kItemRows) * c0;
+  }
+  const size_t tail = (static_cast<size_t>(i) * a.Hq + h) * a.S;
+  const int parts = npre + splits;
+  auto ml_at = [&](int p) -> float2 {
+    return p < npre ? a.part_ml[row + static_cast<long long>(kItemRows) * p]
+                    : a.tail_ml[tail + p - npre];
+  };
+  auto o_at = [&](int p) -> const float* {
+    return (p < npre ? a.part_o + (row + static_cast<long long>(kItemRows) * p) * D
+                     : a.tail_o + (tail + p - npre) * D) +
+           lane * V;
+  };
+  float mx = -INFINITY;
+  for (int p = lane; p < parts; p += 32) mx = fmaxf(mx, ml_at(p).x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  float acc[V], lsum = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int p0 = warp; p0 < parts; p0 += kJoinWarps * kJoinBatch) {
+    float x[kJoinBatch][V];
+    float2 ml[kJoinBatch];
+#pragma unroll
+    for (int e = 0; e < kJoinBatch; ++e) {
+      const int p = p0 + e * kJoinWarps;
+      ml[e] = make_float2(-INFINITY, 0.f);
+      if (p < parts) {
+        ml[e] = ml_at(p);
+        const float* src = o_at(p);
+        if constexpr (V == 4) *reinterpret_cast<float4*>(x[e]) = *reinterpret_cast<const float4*>(src);
+        else *reinterpret_cast<float2*>(x[e]) = *reinterpret_cast<const float2*>(src);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kJoinBatch; ++e) {
+      if (ml[e].x == -INFINITY) continue;
+      const float f = ex2(ml[e].x - mx);
+      lsum += f * ml[e].y;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(f, x[e][v], acc[v]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) red_o[warp][lane * V + v] = acc[v];
+  if (lane == 0) red_l[warp] = lsum;
+  __syncthreads();
+  if (warp != 0) return;
+  float l = 0.f, r[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) r[v] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    l += red_l[w];
+#pragma unroll
+    for (int v = 0; v < V; ++v) r[v] += red_o[w][lane * V + v];
+  }
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // NaN stays NaN
+  __nv_bfloat16* dst = a.out + (static_cast<size_t>(rw.x) * a.Hq + h) * D + lane * V;
+#pragma unroll
+  for (int v = 0; v < V; v += 2)
+    *reinterpret_cast<__nv_bfloat162*>(dst + v) = __floats2bfloat162_rn(r[v] * inv, r[v + 1] * inv);
+}
+
+size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+struct PrefixLayout {
+  size_t head, groups, rows, row_group, part_o, part_ml, tail, total;
+};
+PrefixLayout prefix_layout(int B, int Hq, int D, int max_blocks) {
+  PrefixLayout l;
+  const size_t part_rows = static_cast<size_t>(B) * Hq + static_cast<size_t>(kItemRows) * kMaxCtas;
+  l.head = 0;
+  l.groups = align_up(sizeof(PlanHead));
+  l.rows = align_up(l.groups + static_cast<size_t>(B) * sizeof(PlanGroup));
+  l.row_group = align_up(l.rows + static_cast<size_t>(B) * sizeof(int2));
+  l.part_o = align_up(l.row_group + static_cast<size_t>(B) * sizeof(int));
+  l.part_ml = align_up(l.part_o + part_rows * D * sizeof(float));
+  l.tail = align_up(l.part_ml + part_rows * sizeof(float2));
+  l.total = align_up(l.tail + decode_workspace_bytes(B, Hq, D, max_blocks));
+  return l;
+}
+
+template <int D>
+kara_status launch_prefix_d(const PrefixArgs& a, const PrefixLaunch& L, const DecodeLaunch& tail,
+                            const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+  constexpr size_t smem = PfxSmem<D>::bytes + 1024;
+  static std::atomic<int> ready[kMaxDevices];
+  const int dev = device_slot();
+  if (dev < 0) {
+    set_last_error("paged_prefix_attn", "no usable current CUDA device");
+    return KARA_ERR_CUDA;
+  }
+  if (ready[dev].load() == 0) {
+    if (cudaFuncSetAttribute(prefix_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+      return check_launch("paged_prefix_attn");
+    ready[dev].store(1);
+  }
+  launch_pdl(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+  launch_pdl(prefix_attn_kernel<D>, dim3(static_cast<unsigned>(a.ctas)), dim3(kPfxThreads), smem,
+             stream, tk, tv, a);
+  kara_status st = check_launch("paged_prefix_attn");
+  if (st != KARA_OK) return st;
+  if ((st = launch_decode(tail, stream)) != KARA_OK) return st;
+  launch_pdl(prefix_combine_kernel<D>, dim3(static_cast<unsigned>(a.B * a.Hq)),
+             dim3(32 * kJoinWarps), 0, stream, a);
+  return check_launch("paged_prefix_attn");
+}
+
+}  // namespace
+
+size_t prefix_workspace_bytes(int B, int Hq, int D, int max_blocks) {
+  return prefix_layout(B, Hq, D, max_blocks).total;
+}
+
+kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
+  const PrefixLayout lay = prefix_layout(L.B, L.Hq, L.D, L.max_blocks);
+  uint8_t* ws = static_cast<uint8_t*>(L.workspace);
+  int sms = 148;
+  const int dev = device_slot();
+  if (dev >= 0) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  PrefixArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(L.q);
+  a.block_table = L.block_table;
+  a.ctx_len = L.ctx_len;
+  a.group_ptr = L.group_ptr;
+  a.group_rows = L.group_rows;
+  a.prefix_pages = L.prefix_pages;
+  a.head = reinterpret_cast<PlanHead*>(ws + lay.head);
+  a.groups = reinterpret_cast<PlanGroup*>(ws + lay.groups);
+  a.rows = reinterpret_cast<int2*>(ws + lay.rows);
+  a.row_group = reinterpret_cast<int*>(ws + lay.row_group);
+  a.part_o = reinterpret_cast<float*>(ws + lay.part_o);
+  a.part_ml = reinterpret_cast<float2*>(ws + lay.part_ml);
+  a.S = decode_num_splits(L.max_blocks);
+  float* tail_o = reinterpret_cast<float*>(ws + lay.tail);
+  a.tail_o = tail_o;
+  a.tail_ml = reinterpret_cast<const float2*>(tail_o + static_cast<size_t>(L.B) * L.Hq * a.S * L.D);
+  a.out = static_cast<__nv_bfloat16*>(L.out);
+  a.status = L.status;
+  a.B = L.B;
+  a.Hq = L.Hq;
+  a.Hkv = L.Hkv;
+  a.G = L.Hq / L.Hkv;
+  a.max_blocks = L.max_blocks;
+  a.num_blocks = L.num_blocks;
+  a.num_groups = L.groups;
+  a.extra = L.new_slots;
+  a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  a.negate = L.scale < 0.f ? 1 : 0;
+  a.cs = (a.negate ? -L.scale : L.scale) * 1.4426950408889634f;
+  DecodeLaunch d;
+  d.q = L.q;
+  d.k_cache = L.k_cache;
+  d.v_cache = L.v_cache;
+  d.block_table = L.block_table;
+  d.ctx_len = L.ctx_len;
+  d.out = L.out;
+  d.partial = tail_o;
+  d.status = L.status;
+  d.B = L.B;
+  d.Hq = L.Hq;
+  d.Hkv = L.Hkv;
+  d.D = L.D;
+  d.max_blocks = L.max_blocks;
+  d.num_blocks = L.num_blocks;
+  d.scale = L.scale;
+  d.extra = L.new_slots;
+  d.rows = a.rows;
+  // the same maps as the streaming kernel's: one page of one KV head, 64 channels per box
+  const uint64_t dims[4] = {static_cast<uint64_t>(L.D), static_cast<uint64_t>(L.Hkv), 16,
+                            static_cast<uint64_t>(L.num_blocks)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(L.D) * 2,
+                               static_cast<uint64_t>(L.Hkv) * L.D * 2,
+                               static_cast<uint64_t>(16) * L.Hkv * L.D * 2};
+  CUtensorMap tk, tv;
+  if (!make_bf16_map_4d(&tk, L.k_cache, dims, strides, 16) ||
+      !make_bf16_map_4d(&tv, L.v_cache, dims, strides, 16))
+    return KARA_ERR_CUDA;
+  if (L.D == 128) return launch_prefix_d<128>(a, L, d, tk, tv, stream);
+  if (L.D == 64) return launch_prefix_d<64>(a, L, d, tk, tv, stream);
+  return KARA_ERR_UNSUPPORTED;
+}
+
+}  // namespace kara

@@ -3,7 +3,8 @@ library declared in include/kara.h. Torch provides device memory and the current
 
 The functions carry the C names:
     kara_score, kara_select, kara_token2chunk, kara_compact, paged_decode_attn,
-    lacache_compact, kara_workspace_bytes
+    lacache_compact, kara_workspace_bytes, paged_rope_append, paged_page_bounds,
+    paged_sparse_attn, paged_prefix_attn
 There is no CPU fallback: a missing library raises ``KaraLibraryError``.
 """
 
@@ -28,7 +29,7 @@ ERR_TIMEOUT = 5
 ERR_WORKSPACE = 6
 ERR_BAD_BLOCK = 7
 
-OP_SCORE, OP_COMPACT, OP_DECODE, OP_LACACHE = 1, 2, 3, 4
+OP_SCORE, OP_COMPACT, OP_DECODE, OP_LACACHE, OP_SPARSE, OP_PREFIX = 1, 2, 3, 4, 5, 6
 TRIM_TOKEN, TRIM_CHUNK = 0, 1      # Token2Chunk's trim: token by token, or whole chunks first
 MAX_LAYERS = 128
 
@@ -68,6 +69,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
 
 _SIGNATURES = {
     "kara_score": ([_P, _P, ctypes.POINTER(_Pool), _P, _I, _I, _I, _F, _P, _P, _Z, _P, _P], _I),
@@ -102,6 +104,13 @@ _SIGNATURES = {
     "kara_token2chunk_ex": ([_P, _P, _I, _I, _I, _F, _I, _I, _I, _P, _P], _I),
     "kara_compress": ([_P, ctypes.POINTER(_LayerKV), _I, ctypes.POINTER(_Pool), _P, _I, _I, _I, _F,
                        _I, _I, _P, _P, _Z, _P, _P], _I),
+    "paged_rope_append": ([_P, _P, _P, _L, _L, _L, _I, _P, _P, _P, _I, _I, _P, _P,
+                           ctypes.POINTER(_Pool), _I, _P, _P, _I, _P, _P, _P, _P], _I),
+    "paged_page_bounds": ([_P, ctypes.POINTER(_Pool), _P, _I, _P, _P, _P], _I),
+    "paged_sparse_attn": ([_P, _P, _P, _P, ctypes.POINTER(_Pool), _I, _F, _I, _I, _I, _I, _P, _P,
+                           _P, _Z, _P, _P], _I),
+    "paged_prefix_attn": ([_P, _P, _P, ctypes.POINTER(_Pool), _I, _F, _P, _P, _I, _P, _I, _P, _P,
+                           _Z, _P, _P], _I),
 }
 
 
@@ -611,3 +620,222 @@ def kara_wait_probe(wait_ms: int, status: torch.Tensor | None = None, device="cu
     _check(lib().kara_wait_probe(int(wait_ms), _ptr(status), _stream(stream)), "kara_wait_probe")
     return status
 
+
+
+def _require_shape(t: torch.Tensor, shape, name: str):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _require_cache(pool: PagedPool, **caches):
+    """Pools of one layer, as the pool describes them."""
+    for name, t in caches.items():
+        _require(t, torch.bfloat16, name)
+        _require_shape(t, (pool.num_blocks, pool.page_size, pool.num_kv_heads, pool.head_dim),
+                       name)
+
+
+def _require_heads(t: torch.Tensor, heads: int, d: int, name: str):
+    """[tokens, heads, d] bf16 whose rows are contiguous (any stride between tokens)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}'s heads must be contiguous within a token")
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
+
+
+class _Call:
+    """Device and stream of one call: every tensor on the current device, and what the call
+    allocates (outputs, workspace, status) allocated on the stream that it runs on."""
+
+    def __init__(self, stream, *tensors):
+        devices = {t.device for t in tensors if t is not None}
+        if len(devices) != 1:
+            raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devices))}")
+        self.device = devices.pop()
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {self.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        self.stream = torch.cuda.current_stream() if stream is None else stream
+        if self.stream.device != self.device:
+            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
+        self._ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
+def paged_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, pool: PagedPool, inv_freq: torch.Tensor,
+                      positions: torch.Tensor, cu_tokens: torch.Tensor | None = None,
+                      interleaved: bool = False, bounds: torch.Tensor | None = None,
+                      q_ring: torch.Tensor | None = None, window: int = 0,
+                      q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                      status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """New tokens rotated by position and written behind ctx_len: q [T, Hq, d], k and v
+    [T, Hkv, d] (parts of one projection output are fine), inv_freq fp32 [rotary_dim / 2],
+    positions int32 [T], cu_tokens int32 [B + 1] (None: one token per sequence). Returns the
+    rotated queries [T, Hq, d] (see paged_rope_append in include/kara.h)."""
+    _require_cache(pool, k_cache=k_cache, v_cache=v_cache)
+    hkv, d = pool.num_kv_heads, pool.head_dim
+    batch = int(pool.block_table.shape[0])
+    hq = int(q.shape[1]) if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    _require_heads(q, hq, d, "q")
+    _require_heads(k, hkv, d, "k")
+    _require_heads(v, hkv, d, "v")
+    tokens = int(q.shape[0])
+    if k.shape[0] != tokens or v.shape[0] != tokens:
+        raise ValueError("q, k and v must hold the same tokens")
+    _require(inv_freq, torch.float32, "inv_freq")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rotary_dim / 2]")
+    _require(positions, torch.int32, "positions")
+    _require_shape(positions, (tokens,), "positions")
+    if cu_tokens is not None:
+        _require(cu_tokens, torch.int32, "cu_tokens")
+        _require_shape(cu_tokens, (batch + 1,), "cu_tokens")
+    elif tokens != batch:
+        raise ValueError("without cu_tokens there must be one token per sequence")
+    if bounds is not None:
+        _require(bounds, torch.bfloat16, "bounds")
+        _require_shape(bounds, (pool.num_blocks, hkv, 2, d), "bounds")
+    if q_ring is not None:
+        _require(q_ring, torch.bfloat16, "q_ring")
+        _require_shape(q_ring, (batch, 2 * window, hq, d), "q_ring")
+    ps = pool.c_struct()
+    with _Call(stream, q, k, v, k_cache, v_cache, pool.block_table, inv_freq, positions,
+               cu_tokens, bounds, q_ring, q_out, k_out, status) as call:
+        if q_out is None:
+            q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=call.device)
+        _require(q_out, torch.bfloat16, "q_out")
+        _require_shape(q_out, (tokens, hq, d), "q_out")
+        if k_out is not None:
+            _require(k_out, torch.bfloat16, "k_out")
+            _require_shape(k_out, (tokens, hkv, d), "k_out")
+        status = _status(status, call.device)
+        _check(lib().paged_rope_append(
+            _ptr(q), _ptr(k), _ptr(v), _token_stride(q), _token_stride(k), _token_stride(v),
+            tokens, _ptr(cu_tokens), _ptr(positions), _ptr(inv_freq), 2 * int(inv_freq.numel()),
+            1 if interleaved else 0, _ptr(k_cache), _ptr(v_cache), ctypes.byref(ps), hq,
+            _ptr(bounds), _ptr(q_ring), int(window), _ptr(q_out), _ptr(k_out), _ptr(status),
+            _stream(call.stream)), "paged_rope_append")
+    return q_out
+
+
+def paged_page_bounds(k_cache: torch.Tensor, pool: PagedPool, bounds: torch.Tensor | None = None,
+                      from_slot: torch.Tensor | None = None, new_slots: int = 0,
+                      status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Elementwise minimum and maximum of the keys of complete pages: bounds
+    [num_blocks, Hkv, 2, d] bf16 (a new one starts at zero), for the pages that hold a slot
+    >= from_slot [B] (None: every page)."""
+    _require_cache(pool, k_cache=k_cache)
+    batch = int(pool.block_table.shape[0])
+    shape = (pool.num_blocks, pool.num_kv_heads, 2, pool.head_dim)
+    if from_slot is not None:
+        _require(from_slot, torch.int32, "from_slot")
+        _require_shape(from_slot, (batch,), "from_slot")
+    ps = pool.c_struct()
+    with _Call(stream, k_cache, pool.block_table, bounds, from_slot, status) as call:
+        if bounds is None:
+            bounds = torch.zeros(shape, dtype=torch.bfloat16, device=call.device)
+        _require(bounds, torch.bfloat16, "bounds")
+        _require_shape(bounds, shape, "bounds")
+        status = _status(status, call.device)
+        _check(lib().paged_page_bounds(_ptr(k_cache), ctypes.byref(ps), _ptr(from_slot),
+                                       int(new_slots), _ptr(bounds), _ptr(status),
+                                       _stream(call.stream)), "paged_page_bounds")
+    return bounds
+
+
+def _require_queries(q: torch.Tensor, pool: PagedPool):
+    _require(q, torch.bfloat16, "q")
+    batch = int(pool.block_table.shape[0])
+    if q.dim() != 3 or q.shape[0] != batch or q.shape[2] != pool.head_dim:
+        raise ValueError(f"q must be [{batch}, heads, {pool.head_dim}], got {list(q.shape)}")
+
+
+def paged_sparse_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      bounds: torch.Tensor, pool: PagedPool, num_pages: int,
+                      sink_pages: int = 1, recent_pages: int = 2, new_slots: int = 0,
+                      scale: float | None = None, sel: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One decode step over the num_pages pages of each (sequence, KV head) that the page bounds
+    select: out [B, Hq, d] bf16; sel [B, Hkv, num_pages] int32, if given, gets the pages."""
+    _require_cache(pool, k_cache=k_cache, v_cache=v_cache)
+    _require_queries(q, pool)
+    b, hq, d = q.shape
+    _require(bounds, torch.bfloat16, "bounds")
+    _require_shape(bounds, (pool.num_blocks, pool.num_kv_heads, 2, d), "bounds")
+    if sel is not None:
+        _require(sel, torch.int32, "sel")
+        _require_shape(sel, (b, pool.num_kv_heads, num_pages), "sel")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    ps = pool.c_struct()
+    with _Call(stream, q, k_cache, v_cache, bounds, pool.block_table, sel, out, workspace,
+               status) as call:
+        if out is None:
+            out = torch.empty_like(q)
+        _require(out, torch.bfloat16, "out")
+        _require_shape(out, q.shape, "out")
+        status = _status(status, call.device)
+        nbytes = kara_workspace_bytes(OP_SPARSE, pool, 0, 0, hq, num_pages)
+        ws = _workspace(nbytes, call.device, workspace)
+        _check(lib().paged_sparse_attn(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(bounds), ctypes.byref(ps), hq,
+            float(scale), int(num_pages), int(sink_pages), int(recent_pages), int(new_slots),
+            _ptr(sel), _ptr(out), _ptr(ws), ws.numel(), _ptr(status), _stream(call.stream)),
+            "paged_sparse_attn")
+    return out
+
+
+def paged_prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      pool: PagedPool, group_ptr: torch.Tensor, prefix_pages: torch.Tensor,
+                      group_rows: torch.Tensor | None = None, new_slots: int = 0,
+                      scale: float | None = None, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """One decode step for groups of rows that share their first prefix_pages [groups] pages;
+    group j is the rows (or entries of group_rows [B]) group_ptr[j] .. group_ptr[j+1] - 1.
+    out [B, Hq, d] bf16; rows in no group are not written."""
+    _require_cache(pool, k_cache=k_cache, v_cache=v_cache)
+    _require_queries(q, pool)
+    b, hq, d = q.shape
+    _require(group_ptr, torch.int32, "group_ptr")
+    _require(prefix_pages, torch.int32, "prefix_pages")
+    groups = int(prefix_pages.numel())
+    _require_shape(prefix_pages, (groups,), "prefix_pages")
+    _require_shape(group_ptr, (groups + 1,), "group_ptr")
+    if group_rows is not None:
+        _require(group_rows, torch.int32, "group_rows")
+        _require_shape(group_rows, (b,), "group_rows")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    ps = pool.c_struct()
+    with _Call(stream, q, k_cache, v_cache, pool.block_table, group_ptr, prefix_pages,
+               group_rows, out, workspace, status) as call:
+        if out is None:
+            out = torch.empty_like(q)
+        _require(out, torch.bfloat16, "out")
+        _require_shape(out, q.shape, "out")
+        status = _status(status, call.device)
+        ws = _workspace(kara_workspace_bytes(OP_PREFIX, pool, 0, 0, hq, 0), call.device,
+                        workspace)
+        _check(lib().paged_prefix_attn(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), ctypes.byref(ps), hq, float(scale),
+            _ptr(group_ptr), _ptr(prefix_pages), groups, _ptr(group_rows), int(new_slots),
+            _ptr(out), _ptr(ws), ws.numel(), _ptr(status), _stream(call.stream)),
+            "paged_prefix_attn")
+    return out

@@ -114,7 +114,9 @@ typedef enum kara_op {
   KARA_OP_SCORE = 1,
   KARA_OP_COMPACT = 2,
   KARA_OP_DECODE = 3,
-  KARA_OP_LACACHE = 4
+  KARA_OP_LACACHE = 4,
+  KARA_OP_SPARSE = 5,
+  KARA_OP_PREFIX = 6
 } kara_op;
 
 #define KARA_MAX_LAYERS 128
@@ -333,6 +335,134 @@ kara_status paged_decode_attn(const void* q, const void* k_cache, const void* v_
                               cudaStream_t stream);
 
 /*
+ * paged_rope_append - new tokens enter the paged cache, their queries and keys rotated by
+ * position on the way (rotary position embedding), one token or many per sequence.
+ *
+ * Rotation of the pair (x, y) of channels of pair number i < rotary_dim / 2 at position t:
+ *     a = t * inv_freq[i],   x' = x cos a - y sin a,   y' = y cos a + x sin a
+ * (the product exact enough for any int32 position, the rotation in fp32, rounded once);
+ * channels from rotary_dim on are copied. Pair i is the channels (i, i + rotary_dim / 2), or
+ * (2 i, 2 i + 1) when interleaved != 0. Positions are given, not derived: after a compression
+ * a slot's number is no longer its token's position.
+ *
+ * The tokens are packed: sequence b's are rows cu_tokens[b] .. cu_tokens[b+1] - 1 and take the
+ * slots ctx_len[b], ctx_len[b] + 1, ... (ctx_len is not changed here). cu_tokens NULL: one
+ * token per sequence (num_tokens = batch), the decode step. The blocks of those slots must be
+ * in the table (kara_step_begin for the decode step). The attention calls below then read the
+ * new slots with new_slots > 0, or after ctx_len has been advanced (kara_step_end).
+ *  q          bf16, row t at q + t * q_stride, [num_q_heads, head_dim] contiguous in the row;
+ *  k, v       likewise with num_kv_heads (strides in elements, multiples of 8: the three may be
+ *             parts of one packed projection output).
+ *  cu_tokens  device int32 [batch + 1], ascending from a value >= 0 to at most num_tokens, or
+ *             NULL. Rows before cu_tokens[0] and from cu_tokens[batch] on (padding) are neither
+ *             read nor written.
+ *  positions  device int32 [num_tokens].   inv_freq  device fp32 [rotary_dim / 2].
+ *  rotary_dim a multiple of 16, 16 .. head_dim.
+ *  bounds     bf16 [num_blocks, Hkv, 2, head_dim] or NULL: pages that the call completes get
+ *             their key bounds (as paged_page_bounds).
+ *  q_ring     bf16 [batch, 2*window, num_q_heads, head_dim] or NULL: the rotated query of slot s
+ *             goes to rows s mod window and s mod window + window (the last `window` tokens of
+ *             each sequence).
+ *  q_out      bf16 [num_tokens, num_q_heads, head_dim]; may be q itself when q_stride =
+ *             num_q_heads * head_dim.
+ *  k_out      bf16 [num_tokens, Hkv, head_dim] or NULL: the rotated keys once more, for an
+ *             attention over the prompt itself or kara_decode_append; may be k likewise.
+ *  dev_status KARA_ERR_INVALID_ARG for a descending cu_tokens or one outside [0, num_tokens]
+ *             (that sequence is skipped) or a slot past the table, KARA_ERR_BAD_BLOCK for a block
+ *             id out of range (the token's K and V are then not written, its q_out is).
+ * Sequences that share a block must not append to it in one call.
+ */
+kara_status paged_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int32_t num_tokens,
+                              const int32_t* cu_tokens, const int32_t* positions,
+                              const float* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                              void* k_cache, void* v_cache, const kara_pool* pool,
+                              int32_t num_q_heads, void* bounds, void* q_ring, int32_t window,
+                              void* q_out, void* k_out, int32_t* dev_status,
+                              cudaStream_t stream);
+
+/*
+ * paged_page_bounds - the elementwise minimum and maximum of the keys of complete pages, which
+ * paged_sparse_attn scores:
+ *     bounds[blk][g][0][c] = min over the page's 16 slots of K[blk][slot][g][c], [1]: max.
+ * For every sequence: the pages of slots [0, ctx_len[b] + new_slots) that are complete (16
+ * slots) and hold a slot >= from_slot[b]; other entries of bounds stay as they are. Call it
+ * after the cache was filled, and after kara_compact / lacache_compact with the first rewritten
+ * slot (for kara_compact the window's start, for lacache_compact 0): compaction moves slots to
+ * fresh blocks.
+ *  from_slot  device int32 [batch], or NULL (every page); negative counts as 0.
+ *  bounds     bf16 [num_blocks, Hkv, 2, head_dim]. Keys must not be NaN.
+ *  dev_status KARA_ERR_INVALID_ARG if a length is negative or exceeds the table (the sequence is
+ *             skipped), KARA_ERR_BAD_BLOCK for a block id out of range (the page is skipped).
+ */
+kara_status paged_page_bounds(const void* k_cache, const kara_pool* pool,
+                              const int32_t* from_slot, int32_t new_slots, void* bounds,
+                              int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * paged_sparse_attn - one decode step of grouped-query attention over the pages that matter:
+ * for each sequence and KV head the first sink_pages, the last recent_pages (complete or not)
+ * and the best-scoring of the others, num_pages in all (every page if there are no more).
+ * The score of a page is a bound on the logits its keys can give the group's queries:
+ *     s[b][g][p] = max_h sum_c max(q[b][h][c] lo[p][g][c], q[b][h][c] hi[p][g][c])
+ * over the query heads h of g, (lo, hi) the page's bounds. The selection is that of exact
+ * scores, ties to the lower page. Then, over the slots t of the selected pages P[b][g]:
+ *     out[b][h] = sum_t softmax_t( q[b][h] . K[t][g(h)] * scale ) V[t][g(h)],
+ *                 t < ctx_len[b] + new_slots.
+ *  q, out     bf16 [batch, num_q_heads, head_dim]; an empty context gives a zero row.
+ *  bounds     as from paged_page_bounds, for every complete page; finite.
+ *  scale      > 0.      num_pages >= 1; sink_pages >= 0, recent_pages >= 1, their sum at most
+ *             num_pages.
+ *  new_slots  slots behind ctx_len that are read too (1 inside a decode step, after
+ *             paged_rope_append and before kara_step_end).
+ *  sel        int32 [batch, Hkv, num_pages] or NULL: the selected pages of the sequence
+ *             (ascending), -1 behind them.
+ *  workspace  >= kara_workspace_bytes(KARA_OP_SPARSE, ...).
+ *  dev_status KARA_ERR_INVALID_ARG if a length is negative or exceeds the table,
+ *             KARA_ERR_BAD_BLOCK for a block id out of range (that page's scores and slots are
+ *             skipped).
+ */
+kara_status paged_sparse_attn(const void* q, const void* k_cache, const void* v_cache,
+                              const void* bounds, const kara_pool* pool, int32_t num_q_heads,
+                              float scale, int32_t num_pages, int32_t sink_pages,
+                              int32_t recent_pages, int32_t new_slots, int32_t* sel, void* out,
+                              void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                              cudaStream_t stream);
+
+/*
+ * paged_prefix_attn - one decode step of grouped-query attention for sequences that share their
+ * first pages (many samples of one prompt, requests behind one document): a group's shared
+ * pages are read once for all its rows.
+ *
+ *     out[b][h] = sum_t softmax_t( q[b][h] . K[t][g(h)] * scale ) V[t][g(h)],
+ *                 t < ctx_len[b] + new_slots
+ * as paged_decode_attn. Group j is the rows group_rows[i] (or i itself when group_rows is NULL),
+ * group_ptr[j] <= i < group_ptr[j+1]; their first prefix_pages[j] pages are the same ones and
+ * are read through the table row of the group's first row, the rest through each row's own.
+ * Rows in no group are not computed and their out stays as it was. A row listed twice is
+ * computed twice. A group may be empty or have one row, and share no page.
+ *  group_ptr    device int32 [num_groups + 1], ascending, within [0, batch].
+ *  prefix_pages device int32 [num_groups], whole pages (of 16 slots).
+ *  num_groups   0 .. batch.
+ *  group_rows   device int32 [batch] (entries from group_ptr[num_groups] on are not used) or
+ *               NULL.
+ *  new_slots    as paged_sparse_attn.
+ *  workspace    >= kara_workspace_bytes(KARA_OP_PREFIX, ...).
+ *  dev_status   KARA_ERR_INVALID_ARG for a group_ptr that descends or leaves [0, batch] (the
+ *               group is skipped), a row outside the batch, or a length that is negative, below
+ *               the shared pages or past the table; KARA_ERR_BAD_BLOCK for a block id out of
+ *               range; the outputs of the rows concerned are then unspecified.
+ * Compaction must leave shared pages alone: kara_compact with a window that starts behind them
+ * does, lacache_compact does not.
+ */
+kara_status paged_prefix_attn(const void* q, const void* k_cache, const void* v_cache,
+                              const kara_pool* pool, int32_t num_q_heads, float scale,
+                              const int32_t* group_ptr, const int32_t* prefix_pages,
+                              int32_t num_groups, const int32_t* group_rows, int32_t new_slots,
+                              void* out, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, cudaStream_t stream);
+
+/*
  * The decode loop around the compression calls ([KARA] abstract: compression happens during
  * decoding, on the recently generated context, instead of on a fill threshold; [GIST]
  * section 3 "Der 'Periodische' Zeitplan (KvLLM)": on a fixed schedule, every 100 steps, the
@@ -441,6 +571,9 @@ kara_status lacache_compact(const kara_layer_kv* layers, int32_t num_layers,
  *  KARA_OP_COMPACT: num_seqs, window (the budget k goes in `k_or_budget`).
  *  KARA_OP_DECODE:  pool->batch, num_q_heads, head_dim, max_blocks_per_seq used.
  *  KARA_OP_LACACHE: num_seqs, budget in `k_or_budget`.
+ *  KARA_OP_SPARSE:  pool's batch, num_kv_heads, head_dim, max_blocks_per_seq; num_q_heads;
+ *                   num_pages in `k_or_budget`.
+ *  KARA_OP_PREFIX:  pool's batch, head_dim, max_blocks_per_seq; num_q_heads.
  * `pool` is a host pointer (may be NULL for SCORE).
  */
 size_t kara_workspace_bytes(kara_op op, const kara_pool* pool, int32_t num_seqs, int32_t window,

@@ -21,8 +21,9 @@ Modules:
 * ``lacache`` - the ladder keep map and ladder compaction.
 * ``decode_loop`` - the decode loop around them: block allocation for new slots, the fused
   append + attention step, the tail-W trigger checked periodically, the window-query ring.
+* ``paged_ops`` - rotary append, page key bounds, block-sparse and shared-prefix attention.
 
 Parity status of every function is stated in its module header.
 """
 
-from . import kara, decode, lacache, decode_loop  # noqa: F401
+from . import kara, decode, lacache, decode_loop, paged_ops  # noqa: F401
