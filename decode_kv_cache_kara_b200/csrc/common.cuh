@@ -458,6 +458,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// The same, but NaN if any of them is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Two floats as one fp16x2 word (x in the low half), round to nearest.
 __device__ __forceinline__ uint32_t pack_f16x2(float x, float y) {
   uint32_t r;

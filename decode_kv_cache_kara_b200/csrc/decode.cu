@@ -38,8 +38,9 @@ constexpr int kUnitPages = kDecodeUnitPages;   // pages per work unit (one parti
 //   kAll   every page of sequence b (the block table from page 0 on);
 //   kList  the pages named by a list per (sequence, KV head), ascending (block-sparse
 //          attention: paged_sparse_attn);
-//   kTail  for list position i the cache row rows[i].x from page rows[i].y on (what a row has
-//          behind the pages it shares: paged_prefix_attn); rows[i].x < 0 reads nothing.
+//   kTail  for list position i the cache row rows[i].x from page rows[i].y to slot rows[i].z
+//          (what a row has behind the pages it shares: paged_prefix_attn); its units start at
+//          number rows[i].w, tail_units in all.
 enum class Pages { kAll, kList, kTail };
 
 struct DecodeArgs {
@@ -65,7 +66,8 @@ struct DecodeArgs {
   int extra;                    // slots behind ctx_len that are read as well
   const int32_t* sel;           // kList: [B, Hkv, sel_pages] page numbers
   int sel_pages;
-  const int2* rows;             // kTail: (cache row, first page) per list position
+  const int4* rows;             // kTail: (cache row, first page, slots, first unit)
+  const int* tail_units;
 };
 
 template <int D>
@@ -98,49 +100,78 @@ struct Unit {
   bool ok;
 };
 
+// Unit u for growing u (warp-uniform; every lane calls it). kAll walks the rows; kList gives
+// every (sequence, KV head) the same number of units and passes over those past its pages;
+// kTail searches the rows' first units, 32 at a time.
 template <Pages SRC>
 struct UnitCursor {
   int b = 0, base = 0, per = -1, n = 0, npages = 0;
-  int2 rw = {0, 0};
-  __device__ __forceinline__ Unit seek(const DecodeArgs& a, int u) {
+  __device__ __forceinline__ Unit seek(const DecodeArgs& a, int& u, int stride) {
     Unit x;
     x.ok = false;
-    while (true) {
-      if (b >= a.B) return x;
-      if (per < 0) {
-        if constexpr (SRC == Pages::kTail) {
-          // written by the kernel before the one this may run beside: not through L1
-          rw = __ldcg(a.rows + b);
-          n = rw.x < 0 ? 0 : a.ctx_len[rw.x] + a.extra;
-        } else {
-          n = a.ctx_len[b] + (SRC == Pages::kAll ? 0 : a.extra);
+    if constexpr (SRC == Pages::kAll) {
+      while (true) {
+        if (b >= a.B) return x;
+        if (per < 0) {
+          n = a.ctx_len[b];
+          if (n > a.max_blocks * 16) {
+            report(a.status, KARA_ERR_INVALID_ARG);
+            n = a.max_blocks * 16;
+          }
+          if (n < 0) n = 0;
+          npages = (n + 15) / 16;
+          per = a.Hkv * ((npages + kUnitPages - 1) / kUnitPages);
         }
-        if (n > a.max_blocks * 16) {
-          report(a.status, KARA_ERR_INVALID_ARG);
-          n = a.max_blocks * 16;
-        }
-        if (n < 0) n = 0;
-        npages = (n + 15) / 16;
-        if constexpr (SRC == Pages::kList) npages = min(npages, a.sel_pages);
-        if constexpr (SRC == Pages::kTail) npages = max(npages - rw.y, 0);
-        per = a.Hkv * ((npages + kUnitPages - 1) / kUnitPages);
+        if (u < base + per) break;
+        base += per;
+        ++b;
+        per = -1;
       }
-      if (u < base + per) break;
-      base += per;
-      ++b;
-      per = -1;
-    }
-    const int local = u - base;
-    x.b = b;
-    x.g = local % a.Hkv;
-    x.split = local / a.Hkv;
-    x.n = n;
-    x.p0 = x.split * kUnitPages;
-    x.np = min(kUnitPages, npages - x.p0);
-    x.row = b;
-    if constexpr (SRC == Pages::kTail) {
-      x.p0 += rw.y;
-      x.row = rw.x;
+      const int local = u - base;
+      x.b = b;
+      x.row = b;
+      x.g = local % a.Hkv;
+      x.split = local / a.Hkv;
+      x.n = n;
+      x.p0 = x.split * kUnitPages;
+      x.np = min(kUnitPages, npages - x.p0);
+    } else if constexpr (SRC == Pages::kList) {
+      const int per_row = a.Hkv * a.S;
+      while (true) {
+        x.b = u / per_row;
+        if (x.b >= a.B) return x;
+        const int local = u - x.b * per_row;
+        x.split = local / a.Hkv;
+        x.g = local - x.split * a.Hkv;
+        x.row = x.b;
+        x.n = max(0, min(a.ctx_len[x.b] + a.extra, a.max_blocks * 16));
+        x.p0 = x.split * kUnitPages;
+        x.np = min(kUnitPages, min((x.n + 15) / 16, a.sel_pages) - x.p0);
+        if (x.np > 0) break;
+        u += stride;
+      }
+    } else {
+      // the rows were written by the kernel before the one this runs beside: not through L1
+      if (u >= __ldcg(a.tail_units)) return x;
+      const int lane = lane_id();
+      int lo = 0, len = a.B;                     // rows[lo] starts at or before u
+      while (len > 1) {
+        const int step = (len + 31) >> 5;
+        const int off = lane * step;
+        const bool at = off < len && __ldcg(&a.rows[lo + min(off, len - 1)].w) <= u;
+        const int hit = 31 - __clz(__ballot_sync(0xffffffffu, at));
+        lo += hit * step;
+        len = min(step, len - hit * step);
+      }
+      const int4 r = __ldcg(a.rows + lo);
+      const int local = u - r.w;
+      x.b = lo;
+      x.row = r.x;
+      x.n = r.z;
+      x.split = local / a.Hkv;
+      x.g = local - x.split * a.Hkv;
+      x.p0 = r.y + x.split * kUnitPages;
+      x.np = min(kUnitPages, (r.z + 15) / 16 - x.p0);
     }
     x.ok = true;
     return x;
@@ -223,12 +254,13 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int num_warps = gridDim.x * kDecWarps;
   UnitCursor<SRC> cursor;
   int u = blockIdx.x * kDecWarps + warp;
-  Unit cu = cursor.seek(a, u);
+  Unit cu = cursor.seek(a, u, num_warps);
   if (!cu.ok) {
     if constexpr (SRC == Pages::kTail) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  Unit nu = cursor.seek(a, u + num_warps);
+  u += num_warps;
+  Unit nu = cursor.seek(a, u, num_warps);
 
   // kList: lane j also keeps the page number of the unit's entry j
   auto load_pages = [&](const Unit& x) -> int {
@@ -445,7 +477,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
       qb[ks][1] = qn[ks][1];
     }
     u += num_warps;
-    nu = cursor.seek(a, u + num_warps);
+    nu = cursor.seek(a, u, num_warps);
     pages_nu = load_pages(nu);
     ids_nu = load_ids(nu, pages_nu);
     load_q(nu, qn);
@@ -696,6 +728,7 @@ kara_status launch_decode(const DecodeLaunch& L, cudaStream_t stream) {
   a.sel = L.sel;
   a.sel_pages = L.sel_pages;
   a.rows = L.rows;
+  a.tail_units = L.tail_units;
   const int G = L.Hq / L.Hkv;
   // paged pools as 4-D maps {d, Hkv, 16 slots, blocks}; box = one page of one KV head, 64
   // channels wide, 128-byte swizzle (the same map shape the scoring kernels use)

@@ -155,7 +155,8 @@ struct DecodeLaunch {
   int extra = 0;                   // slots behind ctx_len that are read as well
   const int32_t* sel = nullptr;    // [B, Hkv, sel_pages]
   int sel_pages = 0;
-  const int2* rows = nullptr;      // [B] (cache row or -1, first page)
+  const int4* rows = nullptr;      // [B] (cache row or -1, first page, slots, first unit)
+  const int* tail_units = nullptr; // their number
 };
 // Pages per work unit of the streaming decode kernel: one partial (m, l, o) per unit.
 constexpr int kDecodeUnitPages = 8;

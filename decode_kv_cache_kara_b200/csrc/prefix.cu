@@ -31,20 +31,21 @@ constexpr int kRows = 128;              // query rows per tensor-core tile
 constexpr int kItemRows = 2 * kRows;    // query rows per item: one tile per softmax team
 constexpr int kMaxCtas = 160;           // grid limit (workspace rows are sized by it)
 constexpr int kMinTiles = 2;            // key tiles that are worth a block of their own
+constexpr int kItemCost = 3;            // an item's start and end, in key tiles
 
 // Written by the plan kernel.
 struct PlanHead {
-  long long total;     // key tiles of all items
+  long long total;     // work of all items, in key tiles
   int ctas;            // blocks with prefix work
-  int pad;
+  int tail_units;      // units of the streaming kernel
 };
 struct PlanGroup {
-  long long flat;      // key tiles of the groups before
+  long long flat;      // work of the groups before
   int first, rows;     // list positions [first, first + rows)
   int ktiles;          // key tiles per item (0: no shared part)
   int pages;           // prefix pages
   int row0;            // cache row whose table names the prefix pages
-  int pad;
+  int item_rows;       // query rows per item (fewer in the last)
 };
 
 struct PrefixArgs {
@@ -56,7 +57,7 @@ struct PrefixArgs {
   const int32_t* prefix_pages;
   PlanHead* head;
   PlanGroup* groups;
-  int2* rows;                    // [B]: (cache row or -1, first own page)
+  int4* rows;                    // [B]: (cache row or -1, first own page, slots, first unit)
   int* row_group;                // [B]
   float* part_o;                 // prefix partials: [Hq B + 256 ctas, D]
   float2* part_ml;
@@ -95,7 +96,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
           gr.rows = 0;
         } else if (gr.rows > 1) {
           gr.ktiles = (pages + kTilePages - 1) / kTilePages;
-          len = (gr.rows * a.G + kItemRows - 1) / kItemRows * a.Hkv * gr.ktiles;
+          // even items: their blocks take the same time per key tile
+          const int q = gr.rows * a.G, items_q = (q + kItemRows - 1) / kItemRows;
+          gr.item_rows = (q + items_q - 1) / items_q;
+          len = gr.ktiles == 0 ? 0 : items_q * a.Hkv * (gr.ktiles + kItemCost);
         }
       }
     }
@@ -107,37 +111,53 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     flat += items.start[kPlanThreads];
   }
   if (threadIdx.x == 0) {
-    const long long most = flat / kMinTiles;
+    const long long most = flat / (kMinTiles + kItemCost);
     a.head->total = flat;
     a.head->ctas = static_cast<int>(most < 1 ? 1 : most < a.ctas ? most : a.ctas);
   }
   __syncthreads();               // the groups are written
-  for (int i = threadIdx.x; i < a.B; i += kPlanThreads) {
-    int2 r = make_int2(-1, 0);
-    int lo = 0, hi = a.num_groups;               // ptr[lo] <= i < ptr[hi] where there is one
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.group_ptr[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    const PlanGroup gr = a.groups[lo];
-    if (i >= gr.first && i < gr.first + gr.rows) {
-      const int row = a.group_rows != nullptr ? a.group_rows[i] : i;
-      if (row < 0 || row >= a.B) {
-        report(a.status, KARA_ERR_INVALID_ARG);
-      } else {
-        const int n = a.ctx_len[row];
-        const long long len = static_cast<long long>(n) + a.extra;
-        if (n < 0 || len < static_cast<long long>(gr.pages) * 16 ||
-            len > static_cast<long long>(a.max_blocks) * 16)
+  int units = 0;
+  for (int i0 = 0; i0 < a.B; i0 += kPlanThreads) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    int4 r = make_int4(-1, 0, 0, 0);
+    int mine = 0;
+    if (i < a.B) {
+      int lo = 0, hi = a.num_groups;             // ptr[lo] <= i < ptr[hi] where there is one
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.group_ptr[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      a.row_group[i] = lo;
+      const PlanGroup gr = a.groups[lo];
+      if (i >= gr.first && i < gr.first + gr.rows) {
+        const int row = a.group_rows != nullptr ? a.group_rows[i] : i;
+        if (row < 0 || row >= a.B) {
           report(a.status, KARA_ERR_INVALID_ARG);
-        r = make_int2(row, gr.rows > 1 ? gr.pages : 0);
+        } else {
+          const int n = a.ctx_len[row];
+          const long long len = static_cast<long long>(n) + a.extra;
+          const long long most = static_cast<long long>(a.max_blocks) * 16;
+          if (n < 0 || len < static_cast<long long>(gr.pages) * 16 || len > most)
+            report(a.status, KARA_ERR_INVALID_ARG);
+          r.x = row;
+          r.y = gr.rows > 1 ? gr.pages : 0;
+          r.z = static_cast<int>(len < 0 ? 0 : len > most ? most : len);
+          const int own = max((r.z + 15) / 16 - r.y, 0);
+          mine = a.Hkv * ((own + kDecodeUnitPages - 1) / kDecodeUnitPages);
+        }
       }
     }
-    a.rows[i] = r;
-    a.row_group[i] = lo;
+    row_items_scan(items, mine);
+    r.w = units + items.start[threadIdx.x];
+    if (i < a.B) a.rows[i] = r;
+    units += items.start[kPlanThreads];
   }
+  if (threadIdx.x == 0) a.head->tail_units = units;
 }
+
+// Items of up to kRows query rows go to team 0 alone, larger ones half to each team.
+__device__ __forceinline__ int team0_rows(int rows) { return rows > kRows ? (rows + 1) / 2 : rows; }
 
 // The part of an item that one block works on: key tiles [kt0, kt1).
 struct Seg {
@@ -167,28 +187,35 @@ struct SegCursor {
     j = lo;
   }
   __device__ __forceinline__ bool next(const PrefixArgs& a, Seg& s) {
+    while (true) {
     if (pos >= end) return false;
     PlanGroup gr = a.groups[j];
     while (j + 1 < a.num_groups && a.groups[j + 1].flat <= pos) gr = a.groups[++j];
+    const int cost = gr.ktiles + kItemCost;      // an item's first kItemCost units hold no keys
     const int local = static_cast<int>(pos - gr.flat);
-    const int x = local / gr.ktiles;
+    const int x = local / cost;
     const int t = x / a.Hkv;
+    const int u0 = local - x * cost;
+    const int u1 = static_cast<int>(min(static_cast<long long>(cost), u0 + (end - pos)));
+    pos += u1 - u0;
+    if (u1 <= kItemCost) continue;
     s.g = x - t * a.Hkv;
-    s.kt0 = local - x * gr.ktiles;
-    s.kt1 = static_cast<int>(min(static_cast<long long>(gr.ktiles), s.kt0 + (end - pos)));
+    s.kt0 = max(u0 - kItemCost, 0);
+    s.kt1 = u1 - kItemCost;
     s.first = gr.first;
     s.row0 = gr.row0;
     s.pages = gr.pages;
-    s.q0 = t * kItemRows;
-    s.rows = min(kItemRows, gr.rows * a.G - s.q0);
+    s.q0 = t * gr.item_rows;
+    s.rows = min(gr.item_rows, gr.rows * a.G - s.q0);
     s.out_row = static_cast<long long>(a.Hq) * gr.first + static_cast<long long>(s.q0) * a.Hkv +
                 static_cast<long long>(s.g) * s.rows + static_cast<long long>(kItemRows) * c;
-    pos += s.kt1 - s.kt0;
     return true;
+    }
   }
 };
 
 constexpr int kPfxThreads = 384;        // warp 0: TMA, warp 1: UMMA, warps 4-11: softmax teams
+constexpr int kRegsLow = 72, kRegsHigh = 208;   // registers a thread after the split
 constexpr uint32_t kTmemS = 0;          // S of team w at 128 w; its P (bf16) over S's columns
 constexpr uint32_t kTmemO = 256;        // O of team w at 256 + 128 w
 
@@ -201,7 +228,7 @@ struct PfxSmem {
   static constexpr uint32_t q_off = 0;
   static constexpr uint32_t kv_off = 2 * kTile;
   static constexpr uint32_t bar_off = kv_off + kStages * kTile;
-  static constexpr int kBars = 2 * kStages + 2 * 4 + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 3 + 2 + 2 + 1;
   static constexpr uint32_t bytes = bar_off + kBars * 8 + 16;
 };
 
@@ -220,9 +247,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::bar_off);
   uint64_t* kv_empty = kv_full + kStages;
   uint64_t* q_full = kv_empty + kStages;      // [2] the team's queries are in shared memory
-  uint64_t* s_full = q_full + 2;              // [2]
-  uint64_t* p_full = s_full + 2;              // [2] P written, S read, O rescaled
-  uint64_t* o_full = p_full + 2;              // [2] the segment's products are done
+  uint64_t* s_full = q_full + 2;              // [3] S of team w; [2]: team 0's second buffer
+  uint64_t* p_full = s_full + 3;              // [2] P written, S read, O rescaled
+  uint64_t* o_full = p_full + 2;              // [2] O += P V done
   uint64_t* drained = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -239,6 +266,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       mbar_init(&p_full[w], 4);
       mbar_init(&o_full[w], 1);
     }
+    mbar_init(&s_full[2], 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -260,6 +288,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   cur.init(a, blockIdx.x);
   Seg sg;
 
+  // registers: four warps give up what the eight softmax warps take; the launch has checked that
+  // the block was given that many
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");   // kRegsLow
   if (warp == 0) {
     // ---- TMA producer: K(0), then K(i), V(i - 1), the order of use ----
     if (lane == 0) {
@@ -312,9 +343,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
           mbar_wait(&kv_full[st], ((issued - 1 - st) / kStages) & 1, &give_up, a.status);
     }
   } else if (warp == 1) {
-    // ---- UMMA issuer. Per step i and team w: O_w += P_w(i-1) V(i-1), then S_w(i) = Q_w K(i)^T,
-    // so that one team's products run while the other team exponentiates. S_w(i) overwrites
-    // P_w(i-1) in tensor memory: products execute in issue order. ----
+    // ---- UMMA issuer. Two teams: per step i and team w, O_w += P_w(i-1) V(i-1), then S_w(i) =
+    // Q_w K(i)^T, so that one team's products run while the other team exponentiates; S_w(i)
+    // overwrites P_w(i-1). One team: S(i) goes to the buffers in turn, ahead of O += P(i-1)
+    // V(i-1), so that the team's next tile is ready when it has finished one. Products execute
+    // in issue order. ----
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D) | (1u << 16);   // V is N-major
@@ -331,34 +364,45 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int i = 0; ok && i <= n; ++i) {
           const int k_at = used, v_at = used + (i < n ? 1 : 0);
           const int ks = k_at % kStages, vs = v_at % kStages;
-          if (i < n) ok = mbar_wait(&kv_full[ks], (k_at / kStages) & 1, abort_flag, a.status);
-          if (ok && i > 0)
-            ok = mbar_wait(&kv_full[vs], (v_at / kStages) & 1, abort_flag, a.status);
-          for (int w = 0; ok && w < teams; ++w) {
-            if (i > 0) {
-              ok = mbar_wait(&p_full[w], p_ph[w], abort_flag, a.status);
-              if (!ok) break;
-              p_ph[w] ^= 1;
-              tc_fence_after();
-              const uint32_t v_addr = smem_u32(kv_buf + vs * L::kTile);
+          auto scores = [&](int w, int buf) {   // S = Q_w K(i)^T into buffer buf
+            tc_fence_after();
+            const uint32_t q_addr = smem_u32(q_buf + w * L::kTile);
+            const uint32_t k_addr = smem_u32(kv_buf + ks * L::kTile);
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                umma_bf16_ts(tmem + kTmemO + w * 128, tmem + kTmemS + w * 128 + k * 8,
-                             sw128_mnmajor_desc(v_addr + k * 2048, L::kChunk, 1024), idesc_o,
-                             (i > 1 || k > 0) ? 1u : 0u);
-              if (i == n) umma_commit(&o_full[w]);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * L::kChunk + (k & 3) * 32;
+              umma_bf16(tmem + kTmemS + buf * 128, sw128_kmajor_desc(q_addr + off),
+                        sw128_kmajor_desc(k_addr + off), idesc_s, k > 0 ? 1u : 0u);
             }
-            if (i < n) {
-              tc_fence_after();
-              const uint32_t q_addr = smem_u32(q_buf + w * L::kTile);
-              const uint32_t k_addr = smem_u32(kv_buf + ks * L::kTile);
+          };
+          auto weigh = [&](int w, int buf) -> bool {   // O_w += P(i-1) V(i-1)
+            if (!mbar_wait(&p_full[w], p_ph[w], abort_flag, a.status)) return false;
+            p_ph[w] ^= 1;
+            if (!mbar_wait(&kv_full[vs], (v_at / kStages) & 1, abort_flag, a.status)) return false;
+            tc_fence_after();
+            const uint32_t v_addr = smem_u32(kv_buf + vs * L::kTile);
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * L::kChunk + (k & 3) * 32;
-                umma_bf16(tmem + kTmemS + w * 128, sw128_kmajor_desc(q_addr + off),
-                          sw128_kmajor_desc(k_addr + off), idesc_s, k > 0 ? 1u : 0u);
+            for (int k = 0; k < kKeys / 16; ++k)
+              umma_bf16_ts(tmem + kTmemO + w * 128, tmem + kTmemS + buf * 128 + k * 8,
+                           sw128_mnmajor_desc(v_addr + k * 2048, L::kChunk, 1024), idesc_o,
+                           (i > 1 || k > 0) ? 1u : 0u);
+            umma_commit(&o_full[w]);
+            return true;
+          };
+          if (i < n) ok = mbar_wait(&kv_full[ks], (k_at / kStages) & 1, abort_flag, a.status);
+          if (ok && teams == 1) {
+            if (i < n) {
+              scores(0, i & 1);
+              umma_commit(&s_full[(i & 1) * 2]);
+            }
+            if (i > 0) ok = weigh(0, (i - 1) & 1);
+          } else {
+            for (int w = 0; ok && w < 2; ++w) {
+              if (i > 0) ok = weigh(w, w);
+              if (ok && i < n) {
+                scores(w, w);
+                umma_commit(&s_full[w]);
               }
-              umma_commit(&s_full[w]);
             }
           }
           if (ok && i > 0) umma_commit(&kv_empty[vs]);
@@ -373,33 +417,39 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
     }
   } else if (warp >= 4) {
-    // ---- softmax teams: a thread owns one query row (TMEM lane) ----
+    // ---- softmax teams: a thread owns one query row (TMEM lane) and holds its 128 scores of a
+    // key tile in registers ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");   // kRegsHigh
     const int w = (warp - 4) >> 2;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t s_col = lane_base + kTmemS + w * 128;
     const uint32_t o_col = lane_base + kTmemO + w * 128;
     uint8_t* q_tile = q_buf + w * L::kTile;
     const uint32_t flip = a.negate ? 0x80008000u : 0u;
-    uint32_t s_ph = 0, o_ph = 0;
+    const float2 cs2 = make_float2(a.cs, a.cs);
+    uint32_t s_ph[3] = {0, 0, 0}, o_ph = 0;   // o_ph: parity of the next product to complete
     bool aborted = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       const bool ok = aborted ? false : mbar_wait(bar, parity, abort_flag, a.status);
       aborted = __any_sync(0xffffffffu, !ok) != 0;
     };
     while (!aborted && cur.next(a, sg)) {
-      const int live = sg.rows - w * kRows;     // rows of this team that exist
+      const int half = team0_rows(sg.rows);
+      const int row0 = w == 0 ? 0 : half;       // the team's rows of the item
+      const int live = w == 0 ? half : sg.rows - half;
       if (live <= 0) continue;
+      const bool one_team = sg.rows <= kRows;
       const bool warp_on = quad * 32 < live;
       // the warp's 32 query rows into the swizzled tile, 16 bytes per lane, whole rows at a time
       if (warp_on) {
         constexpr int kPer = D / 8;             // lanes per row
+#pragma unroll 4
         for (int r0 = 0; r0 < 32; r0 += 32 / kPer) {
           const int r = quad * 32 + r0 + lane / kPer, gi = lane % kPer;
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
           if (r < live) {
-            const int qr = sg.q0 + w * kRows + r;
+            const int qr = sg.q0 + row0 + r;
             const int member = qr / a.G, h = qr - member * a.G;
             const int i = sg.first + member;
             int b = a.group_rows != nullptr ? a.group_rows[i] : i;
@@ -421,77 +471,84 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       float m = -INFINITY, l = 0.f;             // m: the exponent base, in units of raw S
       const int n = sg.kt1 - sg.kt0;
       for (int i = 0; i < n; ++i) {
-        wait(&s_full[w], s_ph);
-        s_ph ^= 1;
+        const int buf = one_team ? i & 1 : w;
+        const int bar = one_team ? (i & 1) * 2 : w;
+        wait(&s_full[bar], s_ph[bar]);
+        s_ph[bar] ^= 1;
         if (aborted) break;
+        bool waited = i == 0;                   // for O += P V of step i - 1
         if (warp_on) {
           tc_fence_after();
-          const int valid = min(kKeys, (sg.pages - (sg.kt0 + i) * kTilePages) * 16);
-          float mx = -INFINITY;
+          const uint32_t s_col = lane_base + kTmemS + buf * 128;
+          float v[kKeys];
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
-            float v[32];
-            tmem_ld32(s_col + c, v);
-            tmem_wait_ld();
-            reg_fence<32>(v);
-            if (valid < kKeys) {
+          for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_col + c, v + c);
+          tmem_wait_ld();
+          reg_fence<kKeys>(v);
+          const int valid = (sg.pages - (sg.kt0 + i) * kTilePages) * 16;
+          if (valid < kKeys) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = c + e < valid ? v[e] : -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mx = fmax3(mx, v[e], v[e + 1]);
+            for (int e = 0; e < kKeys; ++e) v[e] = e < valid ? v[e] : -INFINITY;
           }
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < kKeys; e += 8) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) mq[t] = fmax3_nan(mq[t], v[e + 2 * t], v[e + 2 * t + 1]);
+          }
+          const float mx = fmax3_nan(mq[0], mq[1], fmax3_nan(mq[2], mq[3], -INFINITY));
           // the base moves only when the row maximum outgrows it by 2^8 (or on the first tile):
           // weights up to 2^8 lose nothing in fp32 sums and floating bf16
-          const bool move = i == 0 || (mx - m) * a.cs > 8.f;
-          if (i == 0) {
-            m = mx;
-          } else if (__any_sync(0xffffffffu, move)) {
-            // P V(i - 1) is complete: it was issued before S(i)
-            const float to = move ? mx : m;
-            const float f = ex2((m - to) * a.cs);
-            m = to;
-            l *= f;
+          const bool move = i > 0 && !((mx - m) * a.cs <= 8.f);
+          if (i == 0) m = mx;
+          if (__any_sync(0xffffffffu, move)) {
+            if (!waited) wait(&o_full[w], o_ph);   // O is complete up to step i - 1
+            waited = true;
+            if (!aborted) {
+              tc_fence_after();
+              const float to = move ? fmax3_nan(m, mx, mx) : m;
+              const float f = to == m ? 1.f : ex2((m - to) * a.cs);
+              m = to;
+              l *= f;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float v[16];
-              uint32_t u[16];
-              tmem_ld16(o_col + c, v);
-              tmem_wait_ld();
-              reg_fence<16>(v);
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                uint32_t u[16];
+                tmem_ld16(o_col + c, o);
+                tmem_wait_ld();
+                reg_fence<16>(o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * f);
-              tmem_st16(o_col + c, u);
+                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
+                tmem_st16(o_col + c, u);
+              }
             }
           }
-          const float nb = m == -INFINITY ? 0.f : -m * a.cs;
-          float2 sum = make_float2(0.f, 0.f);
+          // m - m: a base of +inf makes the whole row NaN, as it should be
+          const float nb = m == -INFINITY ? 0.f : (m - m) - m * a.cs;
+          const float2 nb2 = make_float2(nb, nb);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < kKeys; c += 32) {
-            float v[32];
             uint32_t u[16];
-            tmem_ld32(s_col + c, v);
-            tmem_wait_ld();
-            reg_fence<32>(v);
-            if (valid < kKeys) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = c + e < valid ? v[e] : -INFINITY;
-            }
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 x = ffma2(make_float2(v[e], v[e + 1]), make_float2(a.cs, a.cs),
-                                     make_float2(nb, nb));
-              const float2 p = make_float2(ex2(x.x), ex2(x.y));
-              sum = fadd2(sum, p);
+              const float2 x = ffma2(make_float2(v[c + e], v[c + e + 1]), cs2, nb2);
+              const float2 p = e % 8 == 6 ? ex2_fma2(x) : make_float2(ex2(x.x), ex2(x.y));
+              sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], p);
               const __nv_bfloat162 pb = __floats2bfloat162_rn(p.x, p.y);
               u[e / 2] = *reinterpret_cast<const uint32_t*>(&pb);
             }
             tmem_st16(s_col + c / 2, u);
           }
-          l += sum.x + sum.y;
+          sum[0] = fadd2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
           tmem_wait_st();
           tc_fence_before();
         }
+        // every product's phase is waited for, so that none is ever two behind
+        if (!waited) wait(&o_full[w], o_ph);
+        if (i > 0) o_ph ^= 1;
+        if (aborted) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[w]);
       }
@@ -501,7 +558,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (aborted) break;
       if (warp_on) {
         tc_fence_after();
-        const size_t r = static_cast<size_t>(sg.out_row) + w * kRows + row;
+        const size_t r = static_cast<size_t>(sg.out_row) + row0 + row;
         if (row < live) a.part_ml[r] = make_float2(m * a.cs, l);
         float* dst = a.part_o + r * D;
 #pragma unroll 1
@@ -544,11 +601,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_combine_kernel(const P
   __shared__ float red_l[kJoinWarps];
   const int i = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
   const int warp = warp_id(), lane = lane_id();
-  const int2 rw = a.rows[i];
+  const int4 rw = a.rows[i];
   if (rw.x < 0) return;                          // not in a group: its output stays as it was
-  int n = a.ctx_len[rw.x] + a.extra;
-  n = max(0, min(n, a.max_blocks * 16));
-  const int own = max((n + 15) / 16 - rw.y, 0);
+  const int own = max((rw.z + 15) / 16 - rw.y, 0);
   const int splits = (own + kDecodeUnitPages - 1) / kDecodeUnitPages;
   // the row's item and the blocks [c0, c0 + npre) that share it
   const PlanGroup gr = a.groups[a.row_group[i]];
@@ -557,15 +612,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_combine_kernel(const P
   if (gr.ktiles > 0) {
     const int g = h / a.G;
     const int qr = (i - gr.first) * a.G + h - g * a.G;
-    const int t = qr / kItemRows, r = qr - t * kItemRows;
-    const int rows_t = min(kItemRows, gr.rows * a.G - t * kItemRows);
-    const long long a0 = gr.flat + static_cast<long long>(t * a.Hkv + g) * gr.ktiles;
+    const int t = qr / gr.item_rows, r = qr - t * gr.item_rows;
+    const int rows_t = min(gr.item_rows, gr.rows * a.G - t * gr.item_rows);
+    // the item's first key is unit a0 of the line
+    const long long a0 = gr.flat + kItemCost +
+                         static_cast<long long>(t * a.Hkv + g) * (gr.ktiles + kItemCost);
     const long long total = a.head->total;
     const int ctas = a.head->ctas;
     c0 = static_cast<int>(((a0 + 1) * ctas - 1) / total);
     npre = static_cast<int>(((a0 + gr.ktiles) * ctas - 1) / total) - c0 + 1;
-    row = static_cast<long long>(a.Hq) * gr.first + static_cast<long long>(t) * kItemRows * a.Hkv +
-          static_cast<long long>(g) * rows_t + r + static_cast<long long>(kItemRows) * c0;
+    row = static_cast<long long>(a.Hq) * gr.first +
+          static_cast<long long>(t) * gr.item_rows * a.Hkv + static_cast<long long>(g) * rows_t +
+          r + static_cast<long long>(kItemRows) * c0;
   }
   const size_t tail = (static_cast<size_t>(i) * a.Hq + h) * a.S;
   const int parts = npre + splits;
@@ -640,7 +698,7 @@ PrefixLayout prefix_layout(int B, int Hq, int D, int max_blocks) {
   l.head = 0;
   l.groups = align_up(sizeof(PlanHead));
   l.rows = align_up(l.groups + static_cast<size_t>(B) * sizeof(PlanGroup));
-  l.row_group = align_up(l.rows + static_cast<size_t>(B) * sizeof(int2));
+  l.row_group = align_up(l.rows + static_cast<size_t>(B) * sizeof(int4));
   l.part_o = align_up(l.row_group + static_cast<size_t>(B) * sizeof(int));
   l.part_ml = align_up(l.part_o + part_rows * D * sizeof(float));
   l.tail = align_up(l.part_ml + part_rows * sizeof(float2));
@@ -662,6 +720,14 @@ kara_status launch_prefix_d(const PrefixArgs& a, const PrefixLaunch& L, const De
     if (cudaFuncSetAttribute(prefix_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
       return check_launch("paged_prefix_attn");
+    // the register split draws on what the block is launched with: more would wait forever
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, prefix_attn_kernel<D>) != cudaSuccess)
+      return check_launch("paged_prefix_attn");
+    if (attr.numRegs * kPfxThreads < 128 * kRegsLow + 256 * kRegsHigh) {
+      set_last_error("paged_prefix_attn", "the kernel was built with too few registers");
+      return KARA_ERR_CUDA;
+    }
     ready[dev].store(1);
   }
   launch_pdl(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
@@ -696,7 +762,7 @@ kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
   a.prefix_pages = L.prefix_pages;
   a.head = reinterpret_cast<PlanHead*>(ws + lay.head);
   a.groups = reinterpret_cast<PlanGroup*>(ws + lay.groups);
-  a.rows = reinterpret_cast<int2*>(ws + lay.rows);
+  a.rows = reinterpret_cast<int4*>(ws + lay.rows);
   a.row_group = reinterpret_cast<int*>(ws + lay.row_group);
   a.part_o = reinterpret_cast<float*>(ws + lay.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + lay.part_ml);
@@ -735,6 +801,7 @@ kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
   d.scale = L.scale;
   d.extra = L.new_slots;
   d.rows = a.rows;
+  d.tail_units = &a.head->tail_units;
   // the same maps as the streaming kernel's: one page of one KV head, 64 channels per box
   const uint64_t dims[4] = {static_cast<uint64_t>(L.D), static_cast<uint64_t>(L.Hkv), 16,
                             static_cast<uint64_t>(L.num_blocks)};

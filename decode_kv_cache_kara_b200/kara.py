@@ -622,58 +622,86 @@ def kara_wait_probe(wait_ms: int, status: torch.Tensor | None = None, device="cu
 
 
 
-def _require_shape(t: torch.Tensor, shape, name: str):
-    if tuple(t.shape) != tuple(shape):
+# ---------------------------------------------------------------------------------------
+# Operators around the paged cache. A decode step makes these calls once per layer, so their
+# checks are written to cost little when they pass: every condition is tested inline and the
+# error text is put together only when one fails.
+# ---------------------------------------------------------------------------------------
+def _check_tensor(t, dtype, shape, name: str) -> int:
+    """A contiguous CUDA tensor of this dtype and shape: its address."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
+            and t.is_contiguous()):
+        _require(t, dtype, name)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
 
 
-def _require_cache(pool: PagedPool, **caches):
-    """Pools of one layer, as the pool describes them."""
-    for name, t in caches.items():
-        _require(t, torch.bfloat16, name)
-        _require_shape(t, (pool.num_blocks, pool.page_size, pool.num_kv_heads, pool.head_dim),
-                       name)
+def _check_optional(t, dtype, shape, name: str):
+    return None if t is None else _check_tensor(t, dtype, shape, name)
 
 
-def _require_heads(t: torch.Tensor, heads: int, d: int, name: str):
-    """[tokens, heads, d] bf16 whose rows are contiguous (any stride between tokens)."""
+def _check_heads(t, heads: int, d: int, name: str) -> int:
+    """[tokens, heads, d] bf16 whose rows are contiguous (any stride between tokens): the
+    stride between its tokens."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(shape)}")
+    row, head, one = t.stride()
+    if (one != 1 or (heads > 1 and head != d)) and shape[0]:
         raise ValueError(f"{name}'s heads must be contiguous within a token")
+    return row if shape[0] > 1 else heads * d
 
 
-def _token_stride(t: torch.Tensor) -> int:
-    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
+def _check_device(stream, tensors) -> int:
+    """Every tensor on the current device, and the stream too: the device's index."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{device}")
+    if stream is not None and stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the current device is "
+                         f"cuda:{device}")
+    return device
 
 
-class _Call:
-    """Device and stream of one call: every tensor on the current device, and what the call
-    allocates (outputs, workspace, status) allocated on the stream that it runs on."""
+def _allocate(stream, fn):
+    """fn() with what it allocates tied to the stream that the call runs on."""
+    if stream is None:
+        return fn()
+    with torch.cuda.stream(stream):
+        return fn()
 
-    def __init__(self, stream, *tensors):
-        devices = {t.device for t in tensors if t is not None}
-        if len(devices) != 1:
-            raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devices))}")
-        self.device = devices.pop()
-        if self.device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {self.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-        self.stream = torch.cuda.current_stream() if stream is None else stream
-        if self.stream.device != self.device:
-            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
-        self._ctx = torch.cuda.stream(self.stream)
 
-    def __enter__(self):
-        self._ctx.__enter__()
-        return self
+def _raw_stream(stream, device: int) -> int:
+    return (torch._C._cuda_getCurrentRawStream(device) if stream is None
+            else stream.cuda_stream)
 
-    def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+
+def _status_ptr(status, stream, device: int):
+    """The status word (a new zeroed one if None) and its address."""
+    if status is None:
+        status = _allocate(stream, lambda: new_status(torch.device("cuda", device)))
+    elif not (isinstance(status, torch.Tensor) and status.is_cuda
+              and status.dtype is torch.int32):
+        _require(status, torch.int32, "status")
+    return status, status.data_ptr()
+
+
+def _workspace_ptr(workspace, nbytes, stream, device: int):
+    """The caller's workspace (its size is checked by the call), or a new one of nbytes()."""
+    if workspace is None:
+        size = max(nbytes(), 256)
+        workspace = _allocate(stream, lambda: torch.empty(
+            size, dtype=torch.uint8, device=torch.device("cuda", device)))
+    elif not (isinstance(workspace, torch.Tensor) and workspace.is_cuda
+              and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
+        _require(workspace, torch.uint8, "workspace")
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def paged_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -687,49 +715,41 @@ def paged_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache
     [T, Hkv, d] (parts of one projection output are fine), inv_freq fp32 [rotary_dim / 2],
     positions int32 [T], cu_tokens int32 [B + 1] (None: one token per sequence). Returns the
     rotated queries [T, Hq, d] (see paged_rope_append in include/kara.h)."""
-    _require_cache(pool, k_cache=k_cache, v_cache=v_cache)
-    hkv, d = pool.num_kv_heads, pool.head_dim
-    batch = int(pool.block_table.shape[0])
-    hq = int(q.shape[1]) if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
-    _require_heads(q, hq, d, "q")
-    _require_heads(k, hkv, d, "k")
-    _require_heads(v, hkv, d, "v")
-    tokens = int(q.shape[0])
+    bf16, int32 = torch.bfloat16, torch.int32
+    hkv, d, nb = pool.num_kv_heads, pool.head_dim, pool.num_blocks
+    cache = (nb, pool.page_size, hkv, d)
+    kc = _check_tensor(k_cache, bf16, cache, "k_cache")
+    vc = _check_tensor(v_cache, bf16, cache, "v_cache")
+    batch = pool.block_table.shape[0]
+    tokens, hq = q.shape[:2] if isinstance(q, torch.Tensor) and q.dim() == 3 else (0, 0)
+    qs, ks = _check_heads(q, hq, d, "q"), _check_heads(k, hkv, d, "k")
+    vs = _check_heads(v, hkv, d, "v")
     if k.shape[0] != tokens or v.shape[0] != tokens:
         raise ValueError("q, k and v must hold the same tokens")
-    _require(inv_freq, torch.float32, "inv_freq")
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rotary_dim / 2]")
-    _require(positions, torch.int32, "positions")
-    _require_shape(positions, (tokens,), "positions")
-    if cu_tokens is not None:
-        _require(cu_tokens, torch.int32, "cu_tokens")
-        _require_shape(cu_tokens, (batch + 1,), "cu_tokens")
-    elif tokens != batch:
+    half = inv_freq.numel() if isinstance(inv_freq, torch.Tensor) else 0
+    fp = _check_tensor(inv_freq, torch.float32, (half,), "inv_freq")
+    pp = _check_tensor(positions, int32, (tokens,), "positions")
+    cp = _check_optional(cu_tokens, int32, (batch + 1,), "cu_tokens")
+    if cp is None and tokens != batch:
         raise ValueError("without cu_tokens there must be one token per sequence")
-    if bounds is not None:
-        _require(bounds, torch.bfloat16, "bounds")
-        _require_shape(bounds, (pool.num_blocks, hkv, 2, d), "bounds")
-    if q_ring is not None:
-        _require(q_ring, torch.bfloat16, "q_ring")
-        _require_shape(q_ring, (batch, 2 * window, hq, d), "q_ring")
+    bp = _check_optional(bounds, bf16, (nb, hkv, 2, d), "bounds")
+    rp = _check_optional(q_ring, bf16, (batch, 2 * window, hq, d), "q_ring")
     ps = pool.c_struct()
-    with _Call(stream, q, k, v, k_cache, v_cache, pool.block_table, inv_freq, positions,
-               cu_tokens, bounds, q_ring, q_out, k_out, status) as call:
-        if q_out is None:
-            q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=call.device)
-        _require(q_out, torch.bfloat16, "q_out")
-        _require_shape(q_out, (tokens, hq, d), "q_out")
-        if k_out is not None:
-            _require(k_out, torch.bfloat16, "k_out")
-            _require_shape(k_out, (tokens, hkv, d), "k_out")
-        status = _status(status, call.device)
-        _check(lib().paged_rope_append(
-            _ptr(q), _ptr(k), _ptr(v), _token_stride(q), _token_stride(k), _token_stride(v),
-            tokens, _ptr(cu_tokens), _ptr(positions), _ptr(inv_freq), 2 * int(inv_freq.numel()),
-            1 if interleaved else 0, _ptr(k_cache), _ptr(v_cache), ctypes.byref(ps), hq,
-            _ptr(bounds), _ptr(q_ring), int(window), _ptr(q_out), _ptr(k_out), _ptr(status),
-            _stream(call.stream)), "paged_rope_append")
+    device = _check_device(stream, (q, k, v, k_cache, v_cache, pool.block_table, pool.ctx_len,
+                                    inv_freq, positions, cu_tokens, bounds, q_ring, q_out, k_out,
+                                    status))
+    if q_out is None:
+        q_out = _allocate(stream, lambda: torch.empty((tokens, hq, d), dtype=bf16,
+                                                      device=q.device))
+    op = _check_tensor(q_out, bf16, (tokens, hq, d), "q_out")
+    kp = _check_optional(k_out, bf16, (tokens, hkv, d), "k_out")
+    status, sp = _status_ptr(status, stream, device)
+    code = lib().paged_rope_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, tokens, cp, pp, fp, 2 * half,
+        1 if interleaved else 0, kc, vc, ps, hq, bp, rp, window, op, kp, sp,
+        _raw_stream(stream, device))
+    if code:
+        raise KaraError(code, "paged_rope_append")
     return q_out
 
 
@@ -739,30 +759,22 @@ def paged_page_bounds(k_cache: torch.Tensor, pool: PagedPool, bounds: torch.Tens
     """Elementwise minimum and maximum of the keys of complete pages: bounds
     [num_blocks, Hkv, 2, d] bf16 (a new one starts at zero), for the pages that hold a slot
     >= from_slot [B] (None: every page)."""
-    _require_cache(pool, k_cache=k_cache)
-    batch = int(pool.block_table.shape[0])
-    shape = (pool.num_blocks, pool.num_kv_heads, 2, pool.head_dim)
-    if from_slot is not None:
-        _require(from_slot, torch.int32, "from_slot")
-        _require_shape(from_slot, (batch,), "from_slot")
+    bf16 = torch.bfloat16
+    hkv, d, nb = pool.num_kv_heads, pool.head_dim, pool.num_blocks
+    kc = _check_tensor(k_cache, bf16, (nb, pool.page_size, hkv, d), "k_cache")
+    fp = _check_optional(from_slot, torch.int32, (pool.block_table.shape[0],), "from_slot")
     ps = pool.c_struct()
-    with _Call(stream, k_cache, pool.block_table, bounds, from_slot, status) as call:
-        if bounds is None:
-            bounds = torch.zeros(shape, dtype=torch.bfloat16, device=call.device)
-        _require(bounds, torch.bfloat16, "bounds")
-        _require_shape(bounds, shape, "bounds")
-        status = _status(status, call.device)
-        _check(lib().paged_page_bounds(_ptr(k_cache), ctypes.byref(ps), _ptr(from_slot),
-                                       int(new_slots), _ptr(bounds), _ptr(status),
-                                       _stream(call.stream)), "paged_page_bounds")
+    device = _check_device(stream, (k_cache, pool.block_table, pool.ctx_len, bounds, from_slot,
+                                    status))
+    shape = (nb, hkv, 2, d)
+    if bounds is None:
+        bounds = _allocate(stream, lambda: torch.zeros(shape, dtype=bf16, device=k_cache.device))
+    bp = _check_tensor(bounds, bf16, shape, "bounds")
+    status, sp = _status_ptr(status, stream, device)
+    code = lib().paged_page_bounds(kc, ps, fp, new_slots, bp, sp, _raw_stream(stream, device))
+    if code:
+        raise KaraError(code, "paged_page_bounds")
     return bounds
-
-
-def _require_queries(q: torch.Tensor, pool: PagedPool):
-    _require(q, torch.bfloat16, "q")
-    batch = int(pool.block_table.shape[0])
-    if q.dim() != 3 or q.shape[0] != batch or q.shape[2] != pool.head_dim:
-        raise ValueError(f"q must be [{batch}, heads, {pool.head_dim}], got {list(q.shape)}")
 
 
 def paged_sparse_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -773,31 +785,31 @@ def paged_sparse_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                       status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """One decode step over the num_pages pages of each (sequence, KV head) that the page bounds
     select: out [B, Hq, d] bf16; sel [B, Hkv, num_pages] int32, if given, gets the pages."""
-    _require_cache(pool, k_cache=k_cache, v_cache=v_cache)
-    _require_queries(q, pool)
-    b, hq, d = q.shape
-    _require(bounds, torch.bfloat16, "bounds")
-    _require_shape(bounds, (pool.num_blocks, pool.num_kv_heads, 2, d), "bounds")
-    if sel is not None:
-        _require(sel, torch.int32, "sel")
-        _require_shape(sel, (b, pool.num_kv_heads, num_pages), "sel")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    bf16 = torch.bfloat16
+    hkv, d, nb = pool.num_kv_heads, pool.head_dim, pool.num_blocks
+    cache = (nb, pool.page_size, hkv, d)
+    kc = _check_tensor(k_cache, bf16, cache, "k_cache")
+    vc = _check_tensor(v_cache, bf16, cache, "v_cache")
+    batch = pool.block_table.shape[0]
+    hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    qp = _check_tensor(q, bf16, (batch, hq, d), "q")
+    bp = _check_tensor(bounds, bf16, (nb, hkv, 2, d), "bounds")
+    lp = _check_optional(sel, torch.int32, (batch, hkv, num_pages), "sel")
     ps = pool.c_struct()
-    with _Call(stream, q, k_cache, v_cache, bounds, pool.block_table, sel, out, workspace,
-               status) as call:
-        if out is None:
-            out = torch.empty_like(q)
-        _require(out, torch.bfloat16, "out")
-        _require_shape(out, q.shape, "out")
-        status = _status(status, call.device)
-        nbytes = kara_workspace_bytes(OP_SPARSE, pool, 0, 0, hq, num_pages)
-        ws = _workspace(nbytes, call.device, workspace)
-        _check(lib().paged_sparse_attn(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(bounds), ctypes.byref(ps), hq,
-            float(scale), int(num_pages), int(sink_pages), int(recent_pages), int(new_slots),
-            _ptr(sel), _ptr(out), _ptr(ws), ws.numel(), _ptr(status), _stream(call.stream)),
-            "paged_sparse_attn")
+    device = _check_device(stream, (q, k_cache, v_cache, bounds, pool.block_table, pool.ctx_len,
+                                    sel, out, workspace, status))
+    if out is None:
+        out = _allocate(stream, lambda: torch.empty_like(q))
+    op = _check_tensor(out, bf16, (batch, hq, d), "out")
+    status, sp = _status_ptr(status, stream, device)
+    workspace, wp, wn = _workspace_ptr(
+        workspace, lambda: lib().kara_workspace_bytes(OP_SPARSE, ps, 0, 0, hq, num_pages), stream,
+        device)
+    code = lib().paged_sparse_attn(
+        qp, kc, vc, bp, ps, hq, 1.0 / math.sqrt(d) if scale is None else scale, num_pages,
+        sink_pages, recent_pages, new_slots, lp, op, wp, wn, sp, _raw_stream(stream, device))
+    if code:
+        raise KaraError(code, "paged_sparse_attn")
     return out
 
 
@@ -810,32 +822,30 @@ def paged_prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     """One decode step for groups of rows that share their first prefix_pages [groups] pages;
     group j is the rows (or entries of group_rows [B]) group_ptr[j] .. group_ptr[j+1] - 1.
     out [B, Hq, d] bf16; rows in no group are not written."""
-    _require_cache(pool, k_cache=k_cache, v_cache=v_cache)
-    _require_queries(q, pool)
-    b, hq, d = q.shape
-    _require(group_ptr, torch.int32, "group_ptr")
-    _require(prefix_pages, torch.int32, "prefix_pages")
-    groups = int(prefix_pages.numel())
-    _require_shape(prefix_pages, (groups,), "prefix_pages")
-    _require_shape(group_ptr, (groups + 1,), "group_ptr")
-    if group_rows is not None:
-        _require(group_rows, torch.int32, "group_rows")
-        _require_shape(group_rows, (b,), "group_rows")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    bf16, int32 = torch.bfloat16, torch.int32
+    hkv, d = pool.num_kv_heads, pool.head_dim
+    cache = (pool.num_blocks, pool.page_size, hkv, d)
+    kc = _check_tensor(k_cache, bf16, cache, "k_cache")
+    vc = _check_tensor(v_cache, bf16, cache, "v_cache")
+    batch = pool.block_table.shape[0]
+    hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    qp = _check_tensor(q, bf16, (batch, hq, d), "q")
+    groups = prefix_pages.numel() if isinstance(prefix_pages, torch.Tensor) else 0
+    pp = _check_tensor(prefix_pages, int32, (groups,), "prefix_pages")
+    gp = _check_tensor(group_ptr, int32, (groups + 1,), "group_ptr")
+    rp = _check_optional(group_rows, int32, (batch,), "group_rows")
     ps = pool.c_struct()
-    with _Call(stream, q, k_cache, v_cache, pool.block_table, group_ptr, prefix_pages,
-               group_rows, out, workspace, status) as call:
-        if out is None:
-            out = torch.empty_like(q)
-        _require(out, torch.bfloat16, "out")
-        _require_shape(out, q.shape, "out")
-        status = _status(status, call.device)
-        ws = _workspace(kara_workspace_bytes(OP_PREFIX, pool, 0, 0, hq, 0), call.device,
-                        workspace)
-        _check(lib().paged_prefix_attn(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), ctypes.byref(ps), hq, float(scale),
-            _ptr(group_ptr), _ptr(prefix_pages), groups, _ptr(group_rows), int(new_slots),
-            _ptr(out), _ptr(ws), ws.numel(), _ptr(status), _stream(call.stream)),
-            "paged_prefix_attn")
+    device = _check_device(stream, (q, k_cache, v_cache, pool.block_table, pool.ctx_len,
+                                    group_ptr, prefix_pages, group_rows, out, workspace, status))
+    if out is None:
+        out = _allocate(stream, lambda: torch.empty_like(q))
+    op = _check_tensor(out, bf16, (batch, hq, d), "out")
+    status, sp = _status_ptr(status, stream, device)
+    workspace, wp, wn = _workspace_ptr(
+        workspace, lambda: lib().kara_workspace_bytes(OP_PREFIX, ps, 0, 0, hq, 0), stream, device)
+    code = lib().paged_prefix_attn(
+        qp, kc, vc, ps, hq, 1.0 / math.sqrt(d) if scale is None else scale, gp, pp, groups, rp,
+        new_slots, op, wp, wn, sp, _raw_stream(stream, device))
+    if code:
+        raise KaraError(code, "paged_prefix_attn")
     return out
