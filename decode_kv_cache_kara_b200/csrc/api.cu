@@ -222,8 +222,8 @@ size_t kara_workspace_bytes(kara_op op, const kara_pool* pool, int32_t num_seqs,
                                     pool->max_blocks_per_seq, k_or_budget);
     case KARA_OP_PREFIX:
       if (pool == nullptr || pool->batch <= 0 || num_q_heads <= 0) return 0;
-      return prefix_workspace_bytes(pool->batch, num_q_heads, pool->head_dim,
-                                    pool->max_blocks_per_seq);
+      return prefix_workspace_bytes(pool->batch, num_q_heads, pool->num_kv_heads,
+                                    pool->head_dim);
     default:
       return 0;
   }

@@ -25,6 +25,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "page_mma.cuh"
 
 namespace kara {
 
@@ -32,16 +33,7 @@ namespace {
 
 constexpr int kDecThreads = 128;
 constexpr int kDecWarps = 4;
-constexpr int kUnitPages = kDecodeUnitPages;   // pages per work unit (one partial per unit)
-
-// What the rows of a call read:
-//   kAll   every page of sequence b (the block table from page 0 on);
-//   kList  the pages named by a list per (sequence, KV head), ascending (block-sparse
-//          attention: paged_sparse_attn);
-//   kTail  for list position i the cache row rows[i].x from page rows[i].y to slot rows[i].z
-//          (what a row has behind the pages it shares: paged_prefix_attn); its units start at
-//          number rows[i].w, tail_units in all.
-enum class Pages { kAll, kList, kTail };
+constexpr int kUnitPages = 8;      // pages per work unit (one partial per unit)
 
 struct DecodeArgs {
   const __nv_bfloat16* q;
@@ -62,16 +54,8 @@ struct DecodeArgs {
   __nv_bfloat16* v_dst;
   __nv_bfloat16* q_ring;        // [B, 2W, Hq, D] or null
   int ring_w;                   // W
-  // the other page sources
-  int extra;                    // slots behind ctx_len that are read as well
-  const int32_t* sel;           // kList: [B, Hkv, sel_pages] page numbers
-  int sel_pages;
-  const int4* rows;             // kTail: (cache row, first page, slots, first unit)
-  const int* tail_units;
 };
 
-template <int D>
-__host__ __device__ constexpr int page_bytes() { return 16 * D * 2; }   // one page, one KV head
 // Two ring shapes with the same bytes in flight per SM: DEEP = 3 CTAs per SM with 4-page rings
 // per warp, else 4 CTAs per SM (128 registers a thread) with 3-page rings.
 template <bool DEEP>
@@ -86,124 +70,47 @@ constexpr size_t stream_smem_bytes() {
          8 * dec_stages<DEEP>() * kDecWarps;
 }
 
-// Byte offset of 16-byte granule `gi` of row `r` in a 128-byte-swizzled 16-row box.
-__device__ __forceinline__ uint32_t sw128(int r, int gi) {
-  return static_cast<uint32_t>(r * 128 + ((gi ^ (r & 7)) << 4));
-}
-
 // Work units (b, split, g), g fastest: split s covers pages [8s, 8s+8) of sequence b. Warps
 // with consecutive unit ids (the warps of one CTA) read the KV heads of the same blocks at about
 // the same time, so each block's DRAM rows are fetched together.
 struct Unit {
-  int b, g, split, n, p0, np;   // np: pages of the unit; p0: its first page (kList: list entry)
-  int row;                      // cache row (= b except for kTail)
+  int b, g, split, n, p0, np;   // np: pages of the unit
   bool ok;
 };
 
-// Unit u for growing u (warp-uniform; every lane calls it). kAll walks the rows; kList gives
-// every (sequence, KV head) the same number of units and passes over those past its pages;
-// kTail searches the rows' first units, 32 at a time.
-template <Pages SRC>
 struct UnitCursor {
   int b = 0, base = 0, per = -1, n = 0, npages = 0;
-  __device__ __forceinline__ Unit seek(const DecodeArgs& a, int& u, int stride) {
+  __device__ __forceinline__ Unit seek(const DecodeArgs& a, int u) {
     Unit x;
     x.ok = false;
-    if constexpr (SRC == Pages::kAll) {
-      while (true) {
-        if (b >= a.B) return x;
-        if (per < 0) {
-          n = a.ctx_len[b];
-          if (n > a.max_blocks * 16) {
-            report(a.status, KARA_ERR_INVALID_ARG);
-            n = a.max_blocks * 16;
-          }
-          if (n < 0) n = 0;
-          npages = (n + 15) / 16;
-          per = a.Hkv * ((npages + kUnitPages - 1) / kUnitPages);
+    while (true) {
+      if (b >= a.B) return x;
+      if (per < 0) {
+        n = a.ctx_len[b];
+        if (n > a.max_blocks * 16) {
+          report(a.status, KARA_ERR_INVALID_ARG);
+          n = a.max_blocks * 16;
         }
-        if (u < base + per) break;
-        base += per;
-        ++b;
-        per = -1;
+        if (n < 0) n = 0;
+        npages = (n + 15) / 16;
+        per = a.Hkv * ((npages + kUnitPages - 1) / kUnitPages);
       }
-      const int local = u - base;
-      x.b = b;
-      x.row = b;
-      x.g = local % a.Hkv;
-      x.split = local / a.Hkv;
-      x.n = n;
-      x.p0 = x.split * kUnitPages;
-      x.np = min(kUnitPages, npages - x.p0);
-    } else if constexpr (SRC == Pages::kList) {
-      const int per_row = a.Hkv * a.S;
-      while (true) {
-        x.b = u / per_row;
-        if (x.b >= a.B) return x;
-        const int local = u - x.b * per_row;
-        x.split = local / a.Hkv;
-        x.g = local - x.split * a.Hkv;
-        x.row = x.b;
-        x.n = max(0, min(a.ctx_len[x.b] + a.extra, a.max_blocks * 16));
-        x.p0 = x.split * kUnitPages;
-        x.np = min(kUnitPages, min((x.n + 15) / 16, a.sel_pages) - x.p0);
-        if (x.np > 0) break;
-        u += stride;
-      }
-    } else {
-      // the rows were written by the kernel before the one this runs beside: not through L1
-      if (u >= __ldcg(a.tail_units)) return x;
-      const int lane = lane_id();
-      int lo = 0, len = a.B;                     // rows[lo] starts at or before u
-      while (len > 1) {
-        const int step = (len + 31) >> 5;
-        const int off = lane * step;
-        const bool at = off < len && __ldcg(&a.rows[lo + min(off, len - 1)].w) <= u;
-        const int hit = 31 - __clz(__ballot_sync(0xffffffffu, at));
-        lo += hit * step;
-        len = min(step, len - hit * step);
-      }
-      const int4 r = __ldcg(a.rows + lo);
-      const int local = u - r.w;
-      x.b = lo;
-      x.row = r.x;
-      x.n = r.z;
-      x.split = local / a.Hkv;
-      x.g = local - x.split * a.Hkv;
-      x.p0 = r.y + x.split * kUnitPages;
-      x.np = min(kUnitPages, (r.z + 15) / 16 - x.p0);
+      if (u < base + per) break;
+      base += per;
+      ++b;
+      per = -1;
     }
+    const int local = u - base;
+    x.b = b;
+    x.g = local % a.Hkv;
+    x.split = local / a.Hkv;
+    x.n = n;
+    x.p0 = x.split * kUnitPages;
+    x.np = min(kUnitPages, npages - x.p0);
     x.ok = true;
     return x;
   }
 };
-
-// ldmatrix / movmatrix / mma.sync helpers (m16n8k16, bf16 inputs, fp32 accumulators).
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 // Persistent, one independent stream per warp: the warp walks units u = warp_id, +num_warps,
 // ...; its TMA ring (dec_stages single pages) streams, per unit, the unit's K pages and then its
@@ -218,15 +125,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // head over the unit fixes the exponent base, so the accumulators are never rescaled. P^T goes
 // to bf16 and, transposed in registers by movmatrix, becomes the B operand of O^T (d x 8) +=
 // V^T (d x 16) P^T (16 x 8), with V^T fragments read by ldmatrix.trans.
-template <int D, int G, bool DEEP, Pages SRC>
+template <int D, int G, bool DEEP>
 __global__ void __launch_bounds__(kDecThreads, dec_min_blocks<DEEP>())
 decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a) {
   static_assert(G <= 8, "at most 8 query heads per KV head");
   constexpr int kStages = dec_stages<DEEP>();
-  // previous kernel done (PDL launch). kTail runs beside the kernel before it and reads nothing
-  // that it writes; it waits for it at its end, so that what follows sees both.
-  if constexpr (SRC != Pages::kTail) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // previous kernel done (PDL launch)
   constexpr int NCH = D / 64;                 // 64-channel chunks per row
   constexpr int KS = D / 16;                  // k-steps of S^T, m-tiles of O^T
   constexpr uint32_t kPage = page_bytes<D>();
@@ -252,26 +157,15 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int num_warps = gridDim.x * kDecWarps;
-  UnitCursor<SRC> cursor;
+  UnitCursor cursor;
   int u = blockIdx.x * kDecWarps + warp;
-  Unit cu = cursor.seek(a, u, num_warps);
-  if (!cu.ok) {
-    if constexpr (SRC == Pages::kTail) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  u += num_warps;
-  Unit nu = cursor.seek(a, u, num_warps);
+  Unit cu = cursor.seek(a, u);
+  if (!cu.ok) return;
+  Unit nu = cursor.seek(a, u + num_warps);
 
-  // kList: lane j also keeps the page number of the unit's entry j
-  auto load_pages = [&](const Unit& x) -> int {
-    if (SRC != Pages::kList || !x.ok || lane >= x.np) return 0;
-    const int p = a.sel[(static_cast<size_t>(x.b) * a.Hkv + x.g) * a.sel_pages + x.p0 + lane];
-    return min(max(p, 0), a.max_blocks - 1);
-  };
-  auto load_ids = [&](const Unit& x, int page) -> int {
+  auto load_ids = [&](const Unit& x) -> int {
     if (!x.ok || lane >= x.np) return -1;
-    int blk = a.block_table[static_cast<size_t>(x.row) * a.max_blocks +
-                            (SRC == Pages::kList ? page : x.p0 + lane)];
+    int blk = a.block_table[static_cast<size_t>(x.b) * a.max_blocks + x.p0 + lane];
     if (blk < 0 || blk >= a.num_blocks) {
       report(a.status, KARA_ERR_BAD_BLOCK);
       blk = -1;
@@ -283,7 +177,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
   auto load_q = [&](const Unit& x, uint32_t (&qb)[KS][2]) {
     const bool row_ok = x.ok && grp < G;
     const uint32_t* qrow = reinterpret_cast<const uint32_t*>(
-        a.q + (static_cast<size_t>(x.ok ? x.row : 0) * a.Hq + x.g * G + (row_ok ? grp : 0)) * D);
+        a.q + (static_cast<size_t>(x.b) * a.Hq + x.g * G + (row_ok ? grp : 0)) * D);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       qb[ks][0] = row_ok ? qrow[ks * 8 + tig] : 0u;
@@ -291,15 +185,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
   };
 
-  int pages_cu = load_pages(cu), pages_nu = load_pages(nu);
-  int ids_cu = load_ids(cu, pages_cu), ids_nu = load_ids(nu, pages_nu);
-  // slots of the unit's page j that the sequence holds (16 except in its last page)
-  auto valid_slots = [&](int j) -> int {
-    if constexpr (SRC == Pages::kList)
-      return min(16, cu.n - __shfl_sync(0xffffffffu, pages_cu, j) * 16);
-    else
-      return min(16, cu.n - (cu.p0 + j) * 16);
-  };
+  int ids_cu = load_ids(cu), ids_nu = load_ids(nu);
   uint32_t qb[KS][2], qn[KS][2];
   load_q(cu, qb);
   load_q(nu, qn);
@@ -373,7 +259,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[0][e] += acc[1][e];
           // acc: (slot grp, heads 2tig, 2tig+1), (slot grp+8, heads 2tig, 2tig+1)
-          const int valid = valid_slots(j);
+          const int valid = min(16, cu.n - (cu.p0 + j) * 16);
           const bool lo_ok = grp < valid, hi_ok = grp + 8 < valid;
           sc[j][0] = lo_ok ? acc[0][0] * a.cs : -INFINITY;
           sc[j][1] = lo_ok ? acc[0][1] * a.cs : -INFINITY;
@@ -419,7 +305,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int blk = __shfl_sync(0xffffffffu, ids_cu, j);
         const uint32_t vst = acquire(ustart + cu.np + j, blk);
         if (vst != 0u) {
-          const int valid = valid_slots(j);
+          const int valid = min(16, cu.n - (cu.p0 + j) * 16);
           // slots past the context may hold any bits (even NaN); P is 0 there, V is zeroed
           const int s_lo = 2 * tig, s_hi = 8 + 2 * tig;
           const uint32_t mlo = (s_lo < valid ? 0xffffu : 0u) | (s_lo + 1 < valid ? 0xffff0000u : 0u);
@@ -469,7 +355,6 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
     ustart += 2 * cu.np;
     cu = nu;
     ids_cu = ids_nu;
-    pages_cu = pages_nu;
     if (!cu.ok) break;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -477,9 +362,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
       qb[ks][1] = qn[ks][1];
     }
     u += num_warps;
-    nu = cursor.seek(a, u, num_warps);
-    pages_nu = load_pages(nu);
-    ids_nu = load_ids(nu, pages_nu);
+    nu = cursor.seek(a, u + num_warps);
+    ids_nu = load_ids(nu);
     load_q(nu, qn);
   }
   if (aborted) {
@@ -488,7 +372,6 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
     for (int st = 0; st < kStages; ++st)
       if ((pending >> st) & 1u) mbar_wait(&my_bars[st], (phase >> st) & 1, &give_up, a.status);
   }
-  if constexpr (SRC == Pages::kTail) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Merge of the split partials of each (sequence, query head): one CTA of kCombWarps warps per
@@ -516,11 +399,9 @@ decode_combine_kernel(const DecodeArgs a, __nv_bfloat16* __restrict__ out) {
   const int bh = blockIdx.x;
   const int warp = warp_id(), lane = lane_id();
   const int b = bh / a.Hq;
-  int n = a.ctx_len[b] + a.extra;
+  int n = a.ctx_len[b];
   n = max(0, min(n, a.max_blocks * 16));
-  int npages = (n + 15) / 16;
-  if (a.sel != nullptr) npages = min(npages, a.sel_pages);
-  const int splits = (npages + kUnitPages - 1) / kUnitPages;
+  const int splits = (((n + 15) / 16) + kUnitPages - 1) / kUnitPages;
   const float2* ml = a.part_ml + static_cast<size_t>(bh) * a.S;
   const float* po = a.part_o + static_cast<size_t>(bh) * a.S * D + lane * V;
   float mx = -INFINITY;
@@ -630,7 +511,7 @@ decode_combine_kernel(const DecodeArgs a, __nv_bfloat16* __restrict__ out) {
   }
 }
 
-template <int D, int G, bool DEEP, Pages SRC>
+template <int D, int G, bool DEEP>
 kara_status launch_dg(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, void* out,
                       cudaStream_t stream) {
   constexpr size_t smem = stream_smem_bytes<D, DEEP>();
@@ -641,17 +522,16 @@ kara_status launch_dg(const DecodeArgs& a, const CUtensorMap& tk, const CUtensor
     return KARA_ERR_CUDA;
   }
   if (per_sm[dev].load() == 0) {
-    cudaFuncSetAttribute(decode_stream_kernel<D, G, DEEP, SRC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(decode_stream_kernel<D, G, DEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          static_cast<int>(smem));
     int n = 0;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_stream_kernel<D, G, DEEP, SRC>, kDecThreads, smem);
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_stream_kernel<D, G, DEEP>, kDecThreads, smem);
     per_sm[dev].store(n > 0 ? n : 1);
   }
   int sms = 148;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  launch_pdl(decode_stream_kernel<D, G, DEEP, SRC>, dim3(per_sm[dev].load() * sms), dim3(kDecThreads), smem,
+  launch_pdl(decode_stream_kernel<D, G, DEEP>, dim3(per_sm[dev].load() * sms), dim3(kDecThreads), smem,
              stream, tk, tv, a);
-  if (SRC == Pages::kTail) return check_launch("paged_prefix_attn");   // its caller combines
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.B * a.Hq);
   cfg.blockDim = dim3(32 * kCombWarps);
@@ -674,25 +554,25 @@ kara_status launch_dg(const DecodeArgs& a, const CUtensorMap& tk, const CUtensor
 template <int D, int G>
 constexpr bool deep_ring() { return D == 128 && G <= 6; }
 
-template <int D, Pages SRC>
+template <int D>
 kara_status launch_d(const DecodeArgs& a, int G, const CUtensorMap& tk, const CUtensorMap& tv,
                      void* out, cudaStream_t stream) {
   switch (G) {
-    case 1: return launch_dg<D, 1, deep_ring<D, 1>(), SRC>(a, tk, tv, out, stream);
-    case 2: return launch_dg<D, 2, deep_ring<D, 2>(), SRC>(a, tk, tv, out, stream);
-    case 3: return launch_dg<D, 3, deep_ring<D, 3>(), SRC>(a, tk, tv, out, stream);
-    case 4: return launch_dg<D, 4, deep_ring<D, 4>(), SRC>(a, tk, tv, out, stream);
-    case 5: return launch_dg<D, 5, deep_ring<D, 5>(), SRC>(a, tk, tv, out, stream);
-    case 6: return launch_dg<D, 6, deep_ring<D, 6>(), SRC>(a, tk, tv, out, stream);
-    case 7: return launch_dg<D, 7, deep_ring<D, 7>(), SRC>(a, tk, tv, out, stream);
-    case 8: return launch_dg<D, 8, deep_ring<D, 8>(), SRC>(a, tk, tv, out, stream);
+    case 1: return launch_dg<D, 1, deep_ring<D, 1>()>(a, tk, tv, out, stream);
+    case 2: return launch_dg<D, 2, deep_ring<D, 2>()>(a, tk, tv, out, stream);
+    case 3: return launch_dg<D, 3, deep_ring<D, 3>()>(a, tk, tv, out, stream);
+    case 4: return launch_dg<D, 4, deep_ring<D, 4>()>(a, tk, tv, out, stream);
+    case 5: return launch_dg<D, 5, deep_ring<D, 5>()>(a, tk, tv, out, stream);
+    case 6: return launch_dg<D, 6, deep_ring<D, 6>()>(a, tk, tv, out, stream);
+    case 7: return launch_dg<D, 7, deep_ring<D, 7>()>(a, tk, tv, out, stream);
+    case 8: return launch_dg<D, 8, deep_ring<D, 8>()>(a, tk, tv, out, stream);
     default: return KARA_ERR_UNSUPPORTED;
   }
 }
 
 }  // namespace
 
-int decode_num_splits(int pages) { return (pages + kUnitPages - 1) / kUnitPages; }
+int decode_num_splits(int max_blocks) { return (max_blocks + kUnitPages - 1) / kUnitPages; }
 
 size_t decode_workspace_bytes(int B, int Hq, int D, int max_blocks) {
   return static_cast<size_t>(B) * Hq * decode_num_splits(max_blocks) * (D + 2) * sizeof(float);
@@ -707,7 +587,7 @@ kara_status launch_decode(const DecodeLaunch& L, cudaStream_t stream) {
   a.block_table = L.block_table;
   a.ctx_len = L.ctx_len;
   // workspace: o rows [B, Hq, S, D] first, then (m, l) pairs [B, Hq, S]
-  a.S = decode_num_splits(L.sel != nullptr ? L.sel_pages : L.max_blocks);
+  a.S = decode_num_splits(L.max_blocks);
   a.part_o = L.partial;
   a.part_ml = reinterpret_cast<float2*>(L.partial + static_cast<size_t>(L.B) * L.Hq * a.S * L.D);
   a.status = L.status;
@@ -724,11 +604,6 @@ kara_status launch_decode(const DecodeLaunch& L, cudaStream_t stream) {
   a.v_dst = static_cast<__nv_bfloat16*>(const_cast<void*>(L.v_cache));
   a.q_ring = static_cast<__nv_bfloat16*>(L.q_ring);
   a.ring_w = L.ring_w;
-  a.extra = L.extra;
-  a.sel = L.sel;
-  a.sel_pages = L.sel_pages;
-  a.rows = L.rows;
-  a.tail_units = L.tail_units;
   const int G = L.Hq / L.Hkv;
   // paged pools as 4-D maps {d, Hkv, 16 slots, blocks}; box = one page of one KV head, 64
   // channels wide, 128-byte swizzle (the same map shape the scoring kernels use)
@@ -740,16 +615,9 @@ kara_status launch_decode(const DecodeLaunch& L, cudaStream_t stream) {
   if (!make_bf16_map_4d(&tk, L.k_cache, dims, strides, 16) ||
       !make_bf16_map_4d(&tv, L.v_cache, dims, strides, 16))
     return KARA_ERR_CUDA;
-  if (L.D != 128 && L.D != 64) return KARA_ERR_UNSUPPORTED;
-  const bool wide = L.D == 128;
-  if (L.rows != nullptr)
-    return wide ? launch_d<128, Pages::kTail>(a, G, tk, tv, L.out, stream)
-                : launch_d<64, Pages::kTail>(a, G, tk, tv, L.out, stream);
-  if (L.sel != nullptr)
-    return wide ? launch_d<128, Pages::kList>(a, G, tk, tv, L.out, stream)
-                : launch_d<64, Pages::kList>(a, G, tk, tv, L.out, stream);
-  return wide ? launch_d<128, Pages::kAll>(a, G, tk, tv, L.out, stream)
-              : launch_d<64, Pages::kAll>(a, G, tk, tv, L.out, stream);
+  if (L.D == 128) return launch_d<128>(a, G, tk, tv, L.out, stream);
+  if (L.D == 64) return launch_d<64>(a, G, tk, tv, L.out, stream);
+  return KARA_ERR_UNSUPPORTED;
 }
 
 }  // namespace kara

@@ -148,19 +148,8 @@ struct DecodeLaunch {
   const void* v_new = nullptr;
   void* q_ring = nullptr;
   int ring_w = 0;
-  // other page sources (at most one of sel and rows): the pages of a list per (sequence, KV
-  // head), or for every list position a cache row and its first page; in the latter case B
-  // counts list positions, only the partials are computed, and the kernel runs beside the one
-  // launched before it (which must not write `rows` and must have waited for its writer)
-  int extra = 0;                   // slots behind ctx_len that are read as well
-  const int32_t* sel = nullptr;    // [B, Hkv, sel_pages]
-  int sel_pages = 0;
-  const int4* rows = nullptr;      // [B] (cache row or -1, first page, slots, first unit)
-  const int* tail_units = nullptr; // their number
 };
-// Pages per work unit of the streaming decode kernel: one partial (m, l, o) per unit.
-constexpr int kDecodeUnitPages = 8;
-int decode_num_splits(int pages);
+int decode_num_splits(int max_blocks);
 size_t decode_workspace_bytes(int B, int Hq, int D, int max_blocks);
 kara_status launch_decode(const DecodeLaunch& L, cudaStream_t stream);
 
@@ -230,7 +219,7 @@ struct PrefixLaunch {
   int groups, new_slots;
   float scale;
 };
-size_t prefix_workspace_bytes(int B, int Hq, int D, int max_blocks);
+size_t prefix_workspace_bytes(int B, int Hq, int Hkv, int D);
 kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream);
 
 kara_status launch_step_begin(const kara_pool* pool, int32_t* dev_status, cudaStream_t stream);

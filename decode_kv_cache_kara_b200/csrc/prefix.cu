@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "paged_plan.cuh"
 #include "row_items.cuh"
 
 namespace kara {
@@ -27,26 +28,12 @@ namespace {
 
 constexpr int kKeys = 128;              // keys per step
 constexpr int kTilePages = kKeys / 16;
+constexpr int kHalfKeys = 96;           // keys whose weights are handed over first
 constexpr int kRows = 128;              // query rows per tensor-core tile
-constexpr int kItemRows = 2 * kRows;    // query rows per item: one tile per softmax team
+static_assert(kItemRows == 2 * kRows, "one tensor-core tile per softmax team");
 constexpr int kMaxCtas = 160;           // grid limit (workspace rows are sized by it)
 constexpr int kMinTiles = 2;            // key tiles that are worth a block of their own
-constexpr int kItemCost = 3;            // an item's start and end, in key tiles
-
-// Written by the plan kernel.
-struct PlanHead {
-  long long total;     // work of all items, in key tiles
-  int ctas;            // blocks with prefix work
-  int tail_units;      // units of the streaming kernel
-};
-struct PlanGroup {
-  long long flat;      // work of the groups before
-  int first, rows;     // list positions [first, first + rows)
-  int ktiles;          // key tiles per item (0: no shared part)
-  int pages;           // prefix pages
-  int row0;            // cache row whose table names the prefix pages
-  int item_rows;       // query rows per item (fewer in the last)
-};
+constexpr int kTailMinPages = 4;         // a row's own pages that are worth a warp
 
 struct PrefixArgs {
   const __nv_bfloat16* q;
@@ -55,17 +42,14 @@ struct PrefixArgs {
   const int32_t* group_ptr;
   const int32_t* group_rows;     // or null: list position = cache row
   const int32_t* prefix_pages;
-  PlanHead* head;
-  PlanGroup* groups;
-  int4* rows;                    // [B]: (cache row or -1, first own page, slots, first unit)
+  PrefixHead* head;
+  PrefixGroup* groups;
+  int4* rows;                    // [B]: the streaming kernel's line
   int* row_group;                // [B]
   float* part_o;                 // prefix partials: [Hq B + 256 ctas, D]
   float2* part_ml;
-  const float* tail_o;           // the streaming kernel's: [B, Hq, S, D]
-  const float2* tail_ml;
-  __nv_bfloat16* out;
   int32_t* status;
-  int B, Hq, Hkv, G, max_blocks, num_blocks, num_groups, extra, S, ctas;
+  int B, Hq, Hkv, G, max_blocks, num_blocks, num_groups, extra, ctas;
   float cs;                      // |scale| * log2(e)
   int negate;                    // scale < 0: the queries' signs are flipped
 };
@@ -80,7 +64,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
   long long flat = 0;
   for (int j0 = 0; j0 < a.num_groups; j0 += kPlanThreads) {
     const int j = j0 + static_cast<int>(threadIdx.x);
-    PlanGroup gr = {};
+    PrefixGroup gr = {};
     int len = 0;
     if (j < a.num_groups) {
       const int lo = a.group_ptr[j], hi = a.group_ptr[j + 1], pages = a.prefix_pages[j];
@@ -116,7 +100,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     a.head->ctas = static_cast<int>(most < 1 ? 1 : most < a.ctas ? most : a.ctas);
   }
   __syncthreads();               // the groups are written
-  int units = 0;
+  int line = 0;
   for (int i0 = 0; i0 < a.B; i0 += kPlanThreads) {
     const int i = i0 + static_cast<int>(threadIdx.x);
     int4 r = make_int4(-1, 0, 0, 0);
@@ -129,7 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
         else hi = mid;
       }
       a.row_group[i] = lo;
-      const PlanGroup gr = a.groups[lo];
+      const PrefixGroup gr = a.groups[lo];
       if (i >= gr.first && i < gr.first + gr.rows) {
         const int row = a.group_rows != nullptr ? a.group_rows[i] : i;
         if (row < 0 || row >= a.B) {
@@ -143,17 +127,33 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
           r.x = row;
           r.y = gr.rows > 1 ? gr.pages : 0;
           r.z = static_cast<int>(len < 0 ? 0 : len > most ? most : len);
-          const int own = max((r.z + 15) / 16 - r.y, 0);
-          mine = a.Hkv * ((own + kDecodeUnitPages - 1) / kDecodeUnitPages);
+          mine = max((r.z + 15) / 16 - r.y, 0);
         }
       }
     }
     row_items_scan(items, mine);
-    r.w = units + items.start[threadIdx.x];
+    r.w = line + items.start[threadIdx.x];
     if (i < a.B) a.rows[i] = r;
-    units += items.start[kPlanThreads];
+    line += items.start[kPlanThreads];
   }
-  if (threadIdx.x == 0) a.head->tail_units = units;
+  if (threadIdx.x == 0) a.head->tail_pages = line;
+}
+
+// 2^x of a pair on the FMA pipe, as ex2_fma2, but NaN for NaN: the power of two is a factor
+// instead of an addition to the bits.
+__device__ __forceinline__ float2 ex2_poly2(float2 x) {
+  x.x = fmax_nan(x.x, -125.0f);
+  x.y = fmax_nan(x.y, -125.0f);
+  const float2 shifter = make_float2(12582912.0f, 12582912.0f);
+  const float2 t = fadd2(x, shifter);
+  const float2 f = fsub2(x, fsub2(t, shifter));
+  float2 p = ffma2(make_float2(0.009570102207362652f, 0.009570102207362652f), f,
+                   make_float2(0.05591785907745361f, 0.05591785907745361f));
+  p = ffma2(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
+  p = ffma2(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+  p = ffma2(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+  return fmul2(p, make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                              __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000)));
 }
 
 // Items of up to kRows query rows go to team 0 alone, larger ones half to each team.
@@ -189,7 +189,7 @@ struct SegCursor {
   __device__ __forceinline__ bool next(const PrefixArgs& a, Seg& s) {
     while (true) {
     if (pos >= end) return false;
-    PlanGroup gr = a.groups[j];
+    PrefixGroup gr = a.groups[j];
     while (j + 1 < a.num_groups && a.groups[j + 1].flat <= pos) gr = a.groups[++j];
     const int cost = gr.ktiles + kItemCost;      // an item's first kItemCost units hold no keys
     const int local = static_cast<int>(pos - gr.flat);
@@ -228,7 +228,7 @@ struct PfxSmem {
   static constexpr uint32_t q_off = 0;
   static constexpr uint32_t kv_off = 2 * kTile;
   static constexpr uint32_t bar_off = kv_off + kStages * kTile;
-  static constexpr int kBars = 2 * kStages + 2 + 3 + 2 + 2 + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 3 + 2 + 2 + 2 + 1;
   static constexpr uint32_t bytes = bar_off + kBars * 8 + 16;
 };
 
@@ -248,7 +248,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   uint64_t* kv_empty = kv_full + kStages;
   uint64_t* q_full = kv_empty + kStages;      // [2] the team's queries are in shared memory
   uint64_t* s_full = q_full + 2;              // [3] S of team w; [2]: team 0's second buffer
-  uint64_t* p_full = s_full + 3;              // [2] P written, S read, O rescaled
+  uint64_t* p_half = s_full + 3;              // [2] P of the first keys, S read, O rescaled
+  uint64_t* p_full = p_half + 2;              // [2] all of P
   uint64_t* o_full = p_full + 2;              // [2] O += P V done
   uint64_t* drained = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
@@ -263,6 +264,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     for (int w = 0; w < 2; ++w) {
       mbar_init(&q_full[w], 4);
       mbar_init(&s_full[w], 1);
+      mbar_init(&p_half[w], 4);
       mbar_init(&p_full[w], 4);
       mbar_init(&o_full[w], 1);
     }
@@ -376,16 +378,21 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
           };
           auto weigh = [&](int w, int buf) -> bool {   // O_w += P(i-1) V(i-1)
-            if (!mbar_wait(&p_full[w], p_ph[w], abort_flag, a.status)) return false;
-            p_ph[w] ^= 1;
             if (!mbar_wait(&kv_full[vs], (v_at / kStages) & 1, abort_flag, a.status)) return false;
-            tc_fence_after();
             const uint32_t v_addr = smem_u32(kv_buf + vs * L::kTile);
+            for (int part = 0; part < 2; ++part) {
+              if (!mbar_wait(part == 0 ? &p_half[w] : &p_full[w], p_ph[w], abort_flag, a.status))
+                return false;
+              tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              umma_bf16_ts(tmem + kTmemO + w * 128, tmem + kTmemS + buf * 128 + k * 8,
-                           sw128_mnmajor_desc(v_addr + k * 2048, L::kChunk, 1024), idesc_o,
-                           (i > 1 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < kKeys / 16; ++k) {
+                if ((k < kHalfKeys / 16) != (part == 0)) continue;
+                umma_bf16_ts(tmem + kTmemO + w * 128, tmem + kTmemS + buf * 128 + k * 8,
+                             sw128_mnmajor_desc(v_addr + k * 2048, L::kChunk, 1024), idesc_o,
+                             (i > 1 || k > 0) ? 1u : 0u);
+              }
+            }
+            p_ph[w] ^= 1;
             umma_commit(&o_full[w]);
             return true;
           };
@@ -444,25 +451,30 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       // the warp's 32 query rows into the swizzled tile, 16 bytes per lane, whole rows at a time
       if (warp_on) {
         constexpr int kPer = D / 8;             // lanes per row
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32; r0 += 32 / kPer) {
-          const int r = quad * 32 + r0 + lane / kPer, gi = lane % kPer;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (r < live) {
-            const int qr = sg.q0 + row0 + r;
-            const int member = qr / a.G, h = qr - member * a.G;
-            const int i = sg.first + member;
-            int b = a.group_rows != nullptr ? a.group_rows[i] : i;
-            b = min(max(b, 0), a.B - 1);        // a bad row is reported by the plan
-            x = *reinterpret_cast<const uint4*>(
-                a.q + (static_cast<size_t>(b) * a.Hq + sg.g * a.G + h) * D + gi * 8);
-            x.x ^= flip;
-            x.y ^= flip;
-            x.z ^= flip;
-            x.w ^= flip;
-          }
+        constexpr int kTurns = kPer;            // 32 rows, 32 / kPer at a time
+        const int gi = lane % kPer, r0 = quad * 32 + lane / kPer;
+        const __nv_bfloat16* src[kTurns];
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+          const int r = r0 + t * (32 / kPer);
+          const int qr = sg.q0 + row0 + min(r, live - 1);
+          const int member = qr / a.G, h = qr - member * a.G;
+          int b = sg.first + member;
+          if (a.group_rows != nullptr) b = min(max(a.group_rows[b], 0), a.B - 1);   // reported
+          src[t] = a.q + (static_cast<size_t>(b) * a.Hq + sg.g * a.G + h) * D + gi * 8;
+        }
+        uint4 x[kTurns];
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) x[t] = *reinterpret_cast<const uint4*>(src[t]);
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+          const int r = r0 + t * (32 / kPer);
+          x[t].x ^= flip;
+          x[t].y ^= flip;
+          x[t].z ^= flip;
+          x[t].w ^= flip;
           *reinterpret_cast<uint4*>(q_tile + (gi >> 3) * L::kChunk + (r >> 3) * 1024 +
-                                    (r & 7) * 128 + (((gi & 7) ^ (r & 7)) << 4)) = x;
+                                    (r & 7) * 128 + (((gi & 7) ^ (r & 7)) << 4)) = x[t];
         }
         fence_proxy_async();
       }
@@ -480,33 +492,37 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (warp_on) {
           tc_fence_after();
           const uint32_t s_col = lane_base + kTmemS + buf * 128;
+          // a chunk's loads are in flight while the chunk before it goes into the row maximum
           float v[kKeys];
-#pragma unroll
-          for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_col + c, v + c);
-          tmem_wait_ld();
-          reg_fence<kKeys>(v);
           const int valid = (sg.pages - (sg.kt0 + i) * kTilePages) * 16;
-          if (valid < kKeys) {
-#pragma unroll
-            for (int e = 0; e < kKeys; ++e) v[e] = e < valid ? v[e] : -INFINITY;
-          }
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tmem_ld32(s_col, v);
 #pragma unroll
-          for (int e = 0; e < kKeys; e += 8) {
+          for (int c = 0; c < kKeys; c += 32) {
+            tmem_wait_ld();
+            reg_fence<32>(v + c);
+            if (c + 32 < kKeys) tmem_ld32(s_col + c + 32, v + c + 32);
+            if (valid < kKeys) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) mq[t] = fmax3_nan(mq[t], v[e + 2 * t], v[e + 2 * t + 1]);
+              for (int e = 0; e < 32; ++e) v[c + e] = c + e < valid ? v[c + e] : -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) mq[t] = fmax3(mq[t], v[c + e + 2 * t], v[c + e + 2 * t + 1]);
+            }
           }
-          const float mx = fmax3_nan(mq[0], mq[1], fmax3_nan(mq[2], mq[3], -INFINITY));
+          const float mx = fmaxf(fmax3(mq[0], mq[1], mq[2]), mq[3]);
           // the base moves only when the row maximum outgrows it by 2^8 (or on the first tile):
           // weights up to 2^8 lose nothing in fp32 sums and floating bf16
-          const bool move = i > 0 && !((mx - m) * a.cs <= 8.f);
+          const bool move = i > 0 && (mx - m) * a.cs > 8.f;
           if (i == 0) m = mx;
           if (__any_sync(0xffffffffu, move)) {
             if (!waited) wait(&o_full[w], o_ph);   // O is complete up to step i - 1
             waited = true;
             if (!aborted) {
               tc_fence_after();
-              const float to = move ? fmax3_nan(m, mx, mx) : m;
+              const float to = move ? mx : m;
               const float f = to == m ? 1.f : ex2((m - to) * a.cs);
               m = to;
               l *= f;
@@ -533,10 +549,16 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 x = ffma2(make_float2(v[c + e], v[c + e + 1]), cs2, nb2);
-              const float2 p = e % 8 == 6 ? ex2_fma2(x) : make_float2(ex2(x.x), ex2(x.y));
+              const float2 p = e % 8 == 6 ? ex2_poly2(x) : make_float2(ex2(x.x), ex2(x.y));
               sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], p);
               const __nv_bfloat162 pb = __floats2bfloat162_rn(p.x, p.y);
               u[e / 2] = *reinterpret_cast<const uint32_t*>(&pb);
+            }
+            if (c == kHalfKeys) {               // the product may start on the first keys
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_half[w]);
             }
             tmem_st16(s_col + c / 2, u);
           }
@@ -547,6 +569,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         // every product's phase is waited for, so that none is ever two behind
         if (!waited) wait(&o_full[w], o_ph);
+        if (!warp_on && lane == 0) mbar_arrive(&p_half[w]);
         if (i > 0) o_ph ^= 1;
         if (aborted) break;
         __syncwarp();
@@ -587,128 +610,30 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
 }
 
-// One block per (list position, query head): the partials of the row's share of the prefix
-// (one per block that worked on its item) and of its own slots (one per 8 pages). Warps take
-// partials in turn, a lane owns D / 32 channels.
-constexpr int kJoinWarps = 4;
-constexpr int kJoinBatch = 4;
-
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) prefix_combine_kernel(const PrefixArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int V = D / 32;
-  __shared__ float red_o[kJoinWarps][D];
-  __shared__ float red_l[kJoinWarps];
-  const int i = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const int warp = warp_id(), lane = lane_id();
-  const int4 rw = a.rows[i];
-  if (rw.x < 0) return;                          // not in a group: its output stays as it was
-  const int own = max((rw.z + 15) / 16 - rw.y, 0);
-  const int splits = (own + kDecodeUnitPages - 1) / kDecodeUnitPages;
-  // the row's item and the blocks [c0, c0 + npre) that share it
-  const PlanGroup gr = a.groups[a.row_group[i]];
-  int c0 = 0, npre = 0;
-  long long row = 0;
-  if (gr.ktiles > 0) {
-    const int g = h / a.G;
-    const int qr = (i - gr.first) * a.G + h - g * a.G;
-    const int t = qr / gr.item_rows, r = qr - t * gr.item_rows;
-    const int rows_t = min(gr.item_rows, gr.rows * a.G - t * gr.item_rows);
-    // the item's first key is unit a0 of the line
-    const long long a0 = gr.flat + kItemCost +
-                         static_cast<long long>(t * a.Hkv + g) * (gr.ktiles + kItemCost);
-    const long long total = a.head->total;
-    const int ctas = a.head->ctas;
-    c0 = static_cast<int>(((a0 + 1) * ctas - 1) / total);
-    npre = static_cast<int>(((a0 + gr.ktiles) * ctas - 1) / total) - c0 + 1;
-    row = static_cast<long long>(a.Hq) * gr.first +
-          static_cast<long long>(t) * gr.item_rows * a.Hkv + static_cast<long long>(g) * rows_t +
-          r + static_cast<long long>(kItemRows) * c0;
-  }
-  const size_t tail = (static_cast<size_t>(i) * a.Hq + h) * a.S;
-  const int parts = npre + splits;
-  auto ml_at = [&](int p) -> float2 {
-    return p < npre ? a.part_ml[row + static_cast<long long>(kItemRows) * p]
-                    : a.tail_ml[tail + p - npre];
-  };
-  auto o_at = [&](int p) -> const float* {
-    return (p < npre ? a.part_o + (row + static_cast<long long>(kItemRows) * p) * D
-                     : a.tail_o + (tail + p - npre) * D) +
-           lane * V;
-  };
-  float mx = -INFINITY;
-  for (int p = lane; p < parts; p += 32) mx = fmaxf(mx, ml_at(p).x);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  float acc[V], lsum = 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  for (int p0 = warp; p0 < parts; p0 += kJoinWarps * kJoinBatch) {
-    float x[kJoinBatch][V];
-    float2 ml[kJoinBatch];
-#pragma unroll
-    for (int e = 0; e < kJoinBatch; ++e) {
-      const int p = p0 + e * kJoinWarps;
-      ml[e] = make_float2(-INFINITY, 0.f);
-      if (p < parts) {
-        ml[e] = ml_at(p);
-        const float* src = o_at(p);
-        if constexpr (V == 4) *reinterpret_cast<float4*>(x[e]) = *reinterpret_cast<const float4*>(src);
-        else *reinterpret_cast<float2*>(x[e]) = *reinterpret_cast<const float2*>(src);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < kJoinBatch; ++e) {
-      if (ml[e].x == -INFINITY) continue;
-      const float f = ex2(ml[e].x - mx);
-      lsum += f * ml[e].y;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(f, x[e][v], acc[v]);
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) red_o[warp][lane * V + v] = acc[v];
-  if (lane == 0) red_l[warp] = lsum;
-  __syncthreads();
-  if (warp != 0) return;
-  float l = 0.f, r[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) r[v] = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    l += red_l[w];
-#pragma unroll
-    for (int v = 0; v < V; ++v) r[v] += red_o[w][lane * V + v];
-  }
-  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // NaN stays NaN
-  __nv_bfloat16* dst = a.out + (static_cast<size_t>(rw.x) * a.Hq + h) * D + lane * V;
-#pragma unroll
-  for (int v = 0; v < V; v += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + v) = __floats2bfloat162_rn(r[v] * inv, r[v + 1] * inv);
-}
-
 size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct PrefixLayout {
-  size_t head, groups, rows, row_group, part_o, part_ml, tail, total;
+  size_t head, groups, rows, row_group, part_o, part_ml, tail_o, tail_ml, total;
 };
-PrefixLayout prefix_layout(int B, int Hq, int D, int max_blocks) {
+PrefixLayout prefix_layout(int B, int Hq, int Hkv, int D) {
   PrefixLayout l;
   const size_t part_rows = static_cast<size_t>(B) * Hq + static_cast<size_t>(kItemRows) * kMaxCtas;
+  const size_t tail_rows = (static_cast<size_t>(B) + stream_max_ranges(Hkv)) * Hq;
   l.head = 0;
-  l.groups = align_up(sizeof(PlanHead));
-  l.rows = align_up(l.groups + static_cast<size_t>(B) * sizeof(PlanGroup));
+  l.groups = align_up(sizeof(PrefixHead));
+  l.rows = align_up(l.groups + static_cast<size_t>(B) * sizeof(PrefixGroup));
   l.row_group = align_up(l.rows + static_cast<size_t>(B) * sizeof(int4));
   l.part_o = align_up(l.row_group + static_cast<size_t>(B) * sizeof(int));
   l.part_ml = align_up(l.part_o + part_rows * D * sizeof(float));
-  l.tail = align_up(l.part_ml + part_rows * sizeof(float2));
-  l.total = align_up(l.tail + decode_workspace_bytes(B, Hq, D, max_blocks));
+  l.tail_o = align_up(l.part_ml + part_rows * sizeof(float2));
+  l.tail_ml = align_up(l.tail_o + tail_rows * D * sizeof(float));
+  l.total = align_up(l.tail_ml + tail_rows * sizeof(float2));
   return l;
 }
 
 template <int D>
-kara_status launch_prefix_d(const PrefixArgs& a, const PrefixLaunch& L, const DecodeLaunch& tail,
-                            const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+kara_status launch_prefix_d(const PrefixArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                            cudaStream_t stream) {
   constexpr size_t smem = PfxSmem<D>::bytes + 1024;
   static std::atomic<int> ready[kMaxDevices];
   const int dev = device_slot();
@@ -733,22 +658,17 @@ kara_status launch_prefix_d(const PrefixArgs& a, const PrefixLaunch& L, const De
   launch_pdl(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
   launch_pdl(prefix_attn_kernel<D>, dim3(static_cast<unsigned>(a.ctas)), dim3(kPfxThreads), smem,
              stream, tk, tv, a);
-  kara_status st = check_launch("paged_prefix_attn");
-  if (st != KARA_OK) return st;
-  if ((st = launch_decode(tail, stream)) != KARA_OK) return st;
-  launch_pdl(prefix_combine_kernel<D>, dim3(static_cast<unsigned>(a.B * a.Hq)),
-             dim3(32 * kJoinWarps), 0, stream, a);
   return check_launch("paged_prefix_attn");
 }
 
 }  // namespace
 
-size_t prefix_workspace_bytes(int B, int Hq, int D, int max_blocks) {
-  return prefix_layout(B, Hq, D, max_blocks).total;
+size_t prefix_workspace_bytes(int B, int Hq, int Hkv, int D) {
+  return prefix_layout(B, Hq, Hkv, D).total;
 }
 
 kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
-  const PrefixLayout lay = prefix_layout(L.B, L.Hq, L.D, L.max_blocks);
+  const PrefixLayout lay = prefix_layout(L.B, L.Hq, L.Hkv, L.D);
   uint8_t* ws = static_cast<uint8_t*>(L.workspace);
   int sms = 148;
   const int dev = device_slot();
@@ -760,17 +680,12 @@ kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
   a.group_ptr = L.group_ptr;
   a.group_rows = L.group_rows;
   a.prefix_pages = L.prefix_pages;
-  a.head = reinterpret_cast<PlanHead*>(ws + lay.head);
-  a.groups = reinterpret_cast<PlanGroup*>(ws + lay.groups);
+  a.head = reinterpret_cast<PrefixHead*>(ws + lay.head);
+  a.groups = reinterpret_cast<PrefixGroup*>(ws + lay.groups);
   a.rows = reinterpret_cast<int4*>(ws + lay.rows);
   a.row_group = reinterpret_cast<int*>(ws + lay.row_group);
   a.part_o = reinterpret_cast<float*>(ws + lay.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + lay.part_ml);
-  a.S = decode_num_splits(L.max_blocks);
-  float* tail_o = reinterpret_cast<float*>(ws + lay.tail);
-  a.tail_o = tail_o;
-  a.tail_ml = reinterpret_cast<const float2*>(tail_o + static_cast<size_t>(L.B) * L.Hq * a.S * L.D);
-  a.out = static_cast<__nv_bfloat16*>(L.out);
   a.status = L.status;
   a.B = L.B;
   a.Hq = L.Hq;
@@ -783,25 +698,6 @@ kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
   a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
   a.negate = L.scale < 0.f ? 1 : 0;
   a.cs = (a.negate ? -L.scale : L.scale) * 1.4426950408889634f;
-  DecodeLaunch d;
-  d.q = L.q;
-  d.k_cache = L.k_cache;
-  d.v_cache = L.v_cache;
-  d.block_table = L.block_table;
-  d.ctx_len = L.ctx_len;
-  d.out = L.out;
-  d.partial = tail_o;
-  d.status = L.status;
-  d.B = L.B;
-  d.Hq = L.Hq;
-  d.Hkv = L.Hkv;
-  d.D = L.D;
-  d.max_blocks = L.max_blocks;
-  d.num_blocks = L.num_blocks;
-  d.scale = L.scale;
-  d.extra = L.new_slots;
-  d.rows = a.rows;
-  d.tail_units = &a.head->tail_units;
   // the same maps as the streaming kernel's: one page of one KV head, 64 channels per box
   const uint64_t dims[4] = {static_cast<uint64_t>(L.D), static_cast<uint64_t>(L.Hkv), 16,
                             static_cast<uint64_t>(L.num_blocks)};
@@ -812,9 +708,47 @@ kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
   if (!make_bf16_map_4d(&tk, L.k_cache, dims, strides, 16) ||
       !make_bf16_map_4d(&tv, L.v_cache, dims, strides, 16))
     return KARA_ERR_CUDA;
-  if (L.D == 128) return launch_prefix_d<128>(a, L, d, tk, tv, stream);
-  if (L.D == 64) return launch_prefix_d<64>(a, L, d, tk, tv, stream);
-  return KARA_ERR_UNSUPPORTED;
+  kara_status st = L.D == 128 ? launch_prefix_d<128>(a, tk, tv, stream)
+                              : launch_prefix_d<64>(a, tk, tv, stream);
+  if (st != KARA_OK) return st;
+  StreamLaunch t;
+  t.q = L.q;
+  t.k_cache = L.k_cache;
+  t.v_cache = L.v_cache;
+  t.block_table = L.block_table;
+  t.status = L.status;
+  t.sel = nullptr;
+  t.sel_pages = 0;
+  t.line.rows = a.rows;
+  t.line.total = &a.head->tail_pages;
+  t.line.max_ranges = 0;
+  t.line.min_pages = kTailMinPages;
+  t.part_o = reinterpret_cast<float*>(ws + lay.tail_o);
+  t.part_ml = reinterpret_cast<float2*>(ws + lay.tail_ml);
+  t.B = L.B;
+  t.Hq = L.Hq;
+  t.Hkv = L.Hkv;
+  t.D = L.D;
+  t.max_blocks = L.max_blocks;
+  t.num_blocks = L.num_blocks;
+  t.scale = L.scale;
+  t.beside = true;
+  if ((st = launch_stream(&t, stream)) != KARA_OK) return st;
+  JoinLaunch j;
+  j.line = t.line;
+  j.part_o = t.part_o;
+  j.part_ml = t.part_ml;
+  j.head = a.head;
+  j.groups = a.groups;
+  j.row_group = a.row_group;
+  j.pre_o = a.part_o;
+  j.pre_ml = a.part_ml;
+  j.out = L.out;
+  j.B = L.B;
+  j.Hq = L.Hq;
+  j.Hkv = L.Hkv;
+  j.D = L.D;
+  return launch_join(j, stream);
 }
 
 }  // namespace kara

@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "paged_plan.cuh"
 #include "row_items.cuh"
 
 namespace kara {
@@ -31,16 +32,22 @@ struct SparseArgs {
   float2* score;        // [B, Hkv, max_blocks]: (score, sum of |terms|)
   int32_t* near_page;   // [B, Hkv, max_blocks]: pages near the border, ascending
   double* near_score;   // [B, Hkv, max_blocks]: their scores in fp64
+  uint32_t* words;      // [B, Hkv, max_blocks / 32]: bitmaps too long for shared memory
   int32_t* sel;         // [B, Hkv, pages]
+  int4* rows;           // [B]: the streaming kernel's line (cache row, 0, slots, start)
+  int* total;
   int32_t* status;
   int B, Hq, Hkv, max_blocks, num_blocks, pages, sink, recent, extra;
 };
 
 // Length of sequence b in slots, and its pages.
-__device__ __forceinline__ int seq_pages(const SparseArgs& a, int b) {
+__device__ __forceinline__ int seq_slots(const SparseArgs& a, int b) {
   const int64_t n = static_cast<int64_t>(a.ctx_len[b]) + a.extra;
   const int64_t top = static_cast<int64_t>(a.max_blocks) * 16;
-  return static_cast<int>(((n < 0 ? 0 : n > top ? top : n) + 15) / 16);
+  return static_cast<int>(n < 0 ? 0 : n > top ? top : n);
+}
+__device__ __forceinline__ int seq_pages(const SparseArgs& a, int b) {
+  return (seq_slots(a, b) + 15) / 16;
 }
 
 __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1,
@@ -55,6 +62,7 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
 
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreBlocks = 3;      // resident blocks per SM
 
 // A warp takes tiles (sequence, 16 pages, KV head): A = the pages' bounds, read straight into
 // fragments, B = the group's queries split by sign. The channel that a fragment slot stands for
@@ -62,7 +70,7 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 // two k-steps) with each load. A second product of the absolute values gives sum |terms|, the
 // scale of the score's error.
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SparseArgs a) {
+__global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) page_score_kernel(const SparseArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int NC = D / 32;                     // 32-channel chunks of a bound row
@@ -72,6 +80,17 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SparseA
   const int G = a.Hq / a.Hkv;
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kScoreWarps + warp;
   const int64_t num_warps = static_cast<int64_t>(gridDim.x) * kScoreWarps;
+  if (blockIdx.x == 0) {                         // the line of selected pages, for the last step
+    int start = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kScoreThreads) {
+      const int bt = b0 + static_cast<int>(threadIdx.x);
+      const int slots = bt < a.B ? seq_slots(a, bt) : 0;
+      row_items_scan(items, min((slots + 15) / 16, a.pages));
+      if (bt < a.B) a.rows[bt] = make_int4(bt, 0, slots, start + items.start[threadIdx.x]);
+      start += items.start[kScoreThreads];
+    }
+    if (threadIdx.x == 0) *a.total = start;
+  }
   int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += kScoreThreads) {
     const int bt = b0 + static_cast<int>(threadIdx.x);
@@ -174,20 +193,28 @@ __device__ __forceinline__ uint64_t order_key(double x) {
   return (b >> 63) ? ~b : b | 0x8000000000000000ull;
 }
 
-constexpr int kSelThreads = 512;
+constexpr int kListMinPages = 2;                 // selected pages that are worth a warp
 constexpr int kSelBits = 11;
 constexpr int kSelBins = 1 << kSelBits;
+constexpr int kSelList = 512;                    // candidates settled by counting
+constexpr int kSelWords = 2048;                  // pages in the shared bitmap, / 32
 
+template <int THREADS>
 struct SelectSmem {
   int hist[kSelBins];
-  int warp_total[kSelThreads / 32];
+  unsigned long long list[kSelList];
+  int list_page[kSelList];
+  uint32_t words[kSelWords];
+  int warp_total[THREADS / 32];
   unsigned long long lo, hi;     // extreme keys
-  int bin, above, total;
+  unsigned long long found;
+  int bin, above, in_bin, total, count, sure, close;
   float err;
 };
 
 // Exclusive prefix sum over the block; s.total gets the sum.
-__device__ __forceinline__ int block_prefix(SelectSmem& s, int v) {
+template <int THREADS>
+__device__ __forceinline__ int block_prefix(SelectSmem<THREADS>& s, int v) {
   const int lane = lane_id(), warp = warp_id();
   int x = v;
 #pragma unroll
@@ -200,7 +227,7 @@ __device__ __forceinline__ int block_prefix(SelectSmem& s, int v) {
   __syncthreads();
   int before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     const int t = s.warp_total[w];
     before += w < warp ? t : 0;
     all += t;
@@ -212,33 +239,11 @@ __device__ __forceinline__ int block_prefix(SelectSmem& s, int v) {
 
 // The k-th largest of the keys key(0 .. n-1), 1 <= k <= n, and how many keys exceed it. Radix
 // selection from the highest bit in which the keys differ (scores of one row share sign and
-// most exponent bits, so the first digit already spreads them over the bins).
-template <typename Key, typename KeyFn>
-__device__ Key kth_largest(SelectSmem& s, int n, int k, const KeyFn& key, int& above) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s.lo = ~0ull;
-    s.hi = 0ull;
-  }
-  __syncthreads();
-  unsigned long long lo = ~0ull, hi = 0ull;
-  for (int i = threadIdx.x; i < n; i += kSelThreads) {
-    const unsigned long long x = key(i);
-    lo = x < lo ? x : lo;
-    hi = x > hi ? x : hi;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const unsigned long long l2 = __shfl_xor_sync(0xffffffffu, lo, off);
-    const unsigned long long h2 = __shfl_xor_sync(0xffffffffu, hi, off);
-    lo = l2 < lo ? l2 : lo;
-    hi = h2 > hi ? h2 : hi;
-  }
-  if (lane_id() == 0) {
-    atomicMin(&s.lo, lo);
-    atomicMax(&s.hi, hi);
-  }
-  __syncthreads();
+// most exponent bits, so the first digit already spreads them over the bins); once a digit's bin
+// holds few keys, those are ranked by counting. s.lo and s.hi hold the extreme keys.
+template <int THREADS, typename KeyFn>
+__device__ unsigned long long kth_largest(SelectSmem<THREADS>& s, int n, int k, const KeyFn& key,
+                                          int& above) {
   const unsigned long long differ = s.lo ^ s.hi;
   int shift = differ == 0 ? 0 : 64 - __clzll(static_cast<long long>(differ));   // bits to settle
   unsigned long long prefix = shift < 64 ? s.hi >> shift : 0ull;                // settled bits
@@ -248,16 +253,18 @@ __device__ Key kth_largest(SelectSmem& s, int n, int k, const KeyFn& key, int& a
     const int bits = min(kSelBits, shift);
     const int next = shift - bits;
     __syncthreads();
-    for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) s.hist[i] = 0;
+    for (int i = threadIdx.x; i < kSelBins; i += THREADS) s.hist[i] = 0;
+    if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kSelThreads) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += THREADS) {
       const unsigned long long x = key(i);
       if ((shift < 64 ? x >> shift : 0ull) == prefix)
         atomicAdd(&s.hist[static_cast<int>(x >> next) & ((1 << bits) - 1)], 1);
     }
     __syncthreads();
-    // bins from the top: thread t holds bins [B - 4(t+1), B - 4t)
-    constexpr int kPer = kSelBins / kSelThreads;
+    // bins from the top: thread t holds the kPer bins below those of the threads before it
+    constexpr int kPer = kSelBins / THREADS;
     int mine[kPer], sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -270,6 +277,7 @@ __device__ Key kth_largest(SelectSmem& s, int n, int k, const KeyFn& key, int& a
       if (run < rest && run + mine[j] >= rest) {
         s.bin = kSelBins - 1 - (static_cast<int>(threadIdx.x) * kPer + j);
         s.above = run;
+        s.in_bin = mine[j];
       }
       run += mine[j];
     }
@@ -278,9 +286,61 @@ __device__ Key kth_largest(SelectSmem& s, int n, int k, const KeyFn& key, int& a
     above += s.above;
     rest -= s.above;
     shift = next;
+    const int in_bin = s.in_bin;
+    if (shift > 0 && in_bin <= min(kSelList, THREADS)) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < n; i += THREADS) {
+        const unsigned long long x = key(i);
+        if (x >> shift == prefix) s.list[atomicAdd(&s.count, 1)] = x;
+      }
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < in_bin) {
+        const unsigned long long x = s.list[threadIdx.x];
+        int more = 0, same = 0;
+        for (int j = 0; j < in_bin; ++j) {
+          more += s.list[j] > x;
+          same += s.list[j] == x;
+        }
+        if (more < rest && more + same >= rest) {   // equal keys write equal values
+          s.found = x;
+          s.above = more;
+        }
+      }
+      __syncthreads();
+      prefix = s.found;
+      above += s.above;
+      shift = 0;
+    }
   }
   __syncthreads();
-  return static_cast<Key>(prefix);
+  return prefix;
+}
+
+// Extreme keys of this thread's keys into s.lo and s.hi (set to the empty range before).
+template <int THREADS>
+__device__ __forceinline__ void merge_extremes(SelectSmem<THREADS>& s, unsigned long long lo,
+                                               unsigned long long hi) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const unsigned long long l2 = __shfl_xor_sync(0xffffffffu, lo, off);
+    const unsigned long long h2 = __shfl_xor_sync(0xffffffffu, hi, off);
+    lo = l2 < lo ? l2 : lo;
+    hi = h2 > hi ? h2 : hi;
+  }
+  if (lane_id() == 0) {
+    atomicMin(&s.lo, lo);
+    atomicMax(&s.hi, hi);
+  }
+}
+// Sets the empty range; ends with a barrier.
+template <int THREADS>
+__device__ __forceinline__ void clear_extremes(SelectSmem<THREADS>& s) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s.lo = ~0ull;
+    s.hi = 0ull;
+  }
+  __syncthreads();
 }
 
 // Error of an fp32 score, relative to the sum of its terms' magnitudes: 2 d <= 256 terms enter
@@ -289,14 +349,51 @@ __device__ Key kth_largest(SelectSmem& s, int n, int k, const KeyFn& key, int& a
 // computed as (|lo| + |hi|) |q| >= them with the same relative error.
 constexpr float kScoreErr = 1.0f / 16384.0f;
 
-// One block per (sequence, KV head). Thread t looks at a run of consecutive pages, so that one
-// prefix sum over the threads orders the output.
+// The largest of the group's exact scores of one page (a warp's work, every lane gets it).
+template <int D>
+__device__ __forceinline__ double exact_score(const SparseArgs& a, int b, int g, int page) {
+  const int G = a.Hq / a.Hkv;
+  const int blk = a.block_table[static_cast<size_t>(b) * a.max_blocks + page];
+  double best = -INFINITY;
+  if (blk < 0 || blk >= a.num_blocks) return best;
+  const __nv_bfloat16* lo = a.bounds + (static_cast<size_t>(blk) * a.Hkv + g) * 2 * D;
+  const __nv_bfloat16* q0 = a.q + (static_cast<size_t>(b) * a.Hq + g * G) * D;
+  float l[D / 32], u[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    l[c] = __bfloat162float(lo[c * 32 + lane_id()]);
+    u[c] = __bfloat162float(lo[D + c * 32 + lane_id()]);
+  }
+#pragma unroll 4
+  for (int h = 0; h < G; ++h) {
+    double sum = 0.0;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const float x = __bfloat162float(q0[h * D + c * 32 + lane_id()]);
+      // a product of two bf16 numbers is exact in fp64 (and in fp32)
+      sum += static_cast<double>(x) * static_cast<double>(x < 0.f ? l[c] : u[c]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    best = sum > best ? sum : best;
+  }
+  return best;
+}
+
+// One block per (sequence, KV head). The chosen pages are a bitmap, so that they come out in
+// ascending order from any order of work.
+// 512 threads: rows of 4K pages (few blocks, long passes) took 8 us less than with 256, 512 rows of
+// 600 pages the same.
+constexpr int kSelThreads = 512;
+
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseArgs a) {
+  constexpr int THREADS = kSelThreads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ SelectSmem s;
+  __shared__ SelectSmem<THREADS> s;
   const int bg = blockIdx.x, b = bg / a.Hkv, g = bg % a.Hkv;
+  const int lane = lane_id();
   const int np = seq_pages(a, b);
   int32_t* sel = a.sel + static_cast<size_t>(bg) * a.pages;
   if (threadIdx.x == 0 && g == 0) {
@@ -305,155 +402,192 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
       report(a.status, KARA_ERR_INVALID_ARG);
   }
   if (np <= a.pages) {                           // everything fits
-    for (int i = threadIdx.x; i < a.pages; i += kSelThreads) sel[i] = i < np ? i : -1;
+    for (int i = threadIdx.x; i < a.pages; i += THREADS) sel[i] = i < np ? i : -1;
     return;
   }
   const int first = a.sink, last = np - a.recent;   // pages [first, last) compete
   const int want = a.pages - a.sink - a.recent;
   const int n = last - first;
   const float2* score = a.score + static_cast<size_t>(bg) * a.max_blocks + first;
+  for (int i = threadIdx.x; i < a.sink; i += THREADS) sel[i] = i;
+  for (int i = threadIdx.x; i < a.recent; i += THREADS) sel[a.sink + want + i] = last + i;
+  if (want == 0) return;
   int32_t* near_page = a.near_page + static_cast<size_t>(bg) * a.max_blocks;
   double* near_score = a.near_score + static_cast<size_t>(bg) * a.max_blocks;
-  for (int i = threadIdx.x; i < a.sink; i += kSelThreads) sel[i] = i;
-  for (int i = threadIdx.x; i < a.recent; i += kSelThreads) sel[a.sink + want + i] = last + i;
-  if (want == 0) return;
+  const int num_words = (n + 31) / 32;
+  uint32_t* words = num_words <= kSelWords
+                        ? s.words
+                        : a.words + static_cast<size_t>(bg) * ((a.max_blocks + 31) / 32);
 
-  // the want-th largest fp32 score, and the error that any score of the row may have
+  // extreme scores and the largest error scale
+  if (threadIdx.x == 0) {
+    s.err = 0.f;
+    s.sure = s.close = 0;
+  }
+  clear_extremes(s);
+  {
+    float err = 0.f;
+    unsigned long long lo = ~0ull, hi = 0ull;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+      const float2 x = score[i];
+      const unsigned long long u = order_key(x.x);
+      lo = u < lo ? u : lo;
+      hi = u > hi ? u : hi;
+      err = x.y == x.y ? fmaxf(err, x.y) : INFINITY;
+    }
+    merge_extremes(s, lo, hi);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, off));
+    if (lane == 0) atomicMax(reinterpret_cast<int*>(&s.err), __float_as_int(err));
+  }
+  __syncthreads();
   int above;
-  const uint32_t tkey = kth_largest<uint32_t>(
-      s, n, want, [&](int i) -> unsigned long long { return order_key(score[i].x); }, above);
+  const uint32_t tkey = static_cast<uint32_t>(kth_largest(
+      s, n, want, [&](int i) -> unsigned long long { return order_key(score[i].x); }, above));
   const float t = tkey == 0u ? __int_as_float(0x7fc00000)
                              : __uint_as_float((tkey & 0x80000000u) ? tkey ^ 0x80000000u : ~tkey);
-  float err = 0.f;
-  if (threadIdx.x == 0) s.err = 0.f;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kSelThreads) {
-    const float e = score[i].y;
-    err = e == e ? fmaxf(err, e) : INFINITY;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-    err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, off));
-  if (lane_id() == 0) atomicMax(reinterpret_cast<int*>(&s.err), __float_as_int(err));
-  __syncthreads();
   const float margin = 2.f * kScoreErr * s.err;
-  // > 0: certainly among the best; < 0: certainly not; 0: near the border
-  auto side = [&](int i) -> int {
-    const float x = score[i].x;
-    return x > t + margin ? 1 : x < t - margin ? -1 : 0;
-  };
-  const int per = (n + kSelThreads - 1) / kSelThreads;
-  const int i0 = min(n, static_cast<int>(threadIdx.x) * per), i1 = min(n, i0 + per);
-  int sure = 0, close = 0;
-  for (int i = i0; i < i1; ++i) {
-    const int c = side(i);
-    sure += c > 0;
-    close += c == 0;
-  }
-  block_prefix(s, sure);
-  const int rest = want - s.total;               // places left for the close ones
-  const int close0 = block_prefix(s, close);
-  const int num_close = s.total;
-  // close pages in ascending order; scored in fp64 unless all of them are wanted
-  uint64_t tc = 0;
-  int ties = num_close;                          // how many equal to tc are taken
-  const bool judge = rest < num_close;
-  if (judge) {
-    int at = close0;
-    for (int i = i0; i < i1; ++i)
-      if (side(i) == 0) near_page[at++] = first + i;
-    __syncthreads();
-    const int G = a.Hq / a.Hkv;
-    for (int j = warp_id(); j < num_close; j += kSelThreads / 32) {
-      const int page = near_page[j];
-      const int blk = a.block_table[static_cast<size_t>(b) * a.max_blocks + page];
-      double best = -INFINITY;
-      if (blk >= 0 && blk < a.num_blocks) {
-        const __nv_bfloat16* lo = a.bounds + (static_cast<size_t>(blk) * a.Hkv + g) * 2 * D;
-        for (int h = 0; h < G; ++h) {
-          const __nv_bfloat16* q = a.q + (static_cast<size_t>(b) * a.Hq + g * G + h) * D;
-          double sum = 0.0;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const int d = c * 32 + lane_id();
-            const float x = __bfloat162float(q[d]);
-            const float y = __bfloat162float(x < 0.f ? lo[d] : lo[D + d]);
-            // a product of two bf16 numbers is exact in fp64
-            sum += static_cast<double>(x) * static_cast<double>(y);
-          }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-          best = sum > best ? sum : best;
-        }
-      }
-      if (lane_id() == 0) near_score[j] = best;
+  // every page: surely among the best, surely not, or near the border
+  for (int i0 = threadIdx.x - lane; i0 < num_words * 32; i0 += THREADS) {
+    const int i = i0 + lane;
+    bool sure = false, close = false;
+    if (i < n) {
+      const float x = score[i].x;
+      sure = x > t + margin;
+      close = !sure && !(x < t - margin);
     }
+    const uint32_t ws = __ballot_sync(0xffffffffu, sure), wc = __ballot_sync(0xffffffffu, close);
+    if (lane == 0) {
+      words[i0 / 32] = ws;
+      if (ws != 0) atomicAdd(&s.sure, __popc(ws));
+    }
+    if (wc != 0) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&s.close, __popc(wc));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(wc & ((1u << lane) - 1));
+      if (close) {
+        if (at < kSelList) s.list_page[at] = i;
+        near_page[at] = i;
+      }
+    }
+  }
+  __syncthreads();
+  const int num_close = s.close, rest = want - s.sure;   // places left for the close pages
+  if (rest >= num_close) {                       // all of them
+    for (int j = threadIdx.x; j < num_close; j += THREADS) {
+      const int i = near_page[j];
+      atomicOr(&words[i / 32], 1u << (i & 31));
+    }
+  } else if (num_close <= min(kSelList, THREADS)) {
+    for (int j = warp_id(); j < num_close; j += THREADS / 32) {
+      const unsigned long long x = order_key(exact_score<D>(a, b, g, first + s.list_page[j]));
+      if (lane == 0) s.list[j] = x;
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < num_close) {
+      const int i = s.list_page[threadIdx.x];
+      const unsigned long long x = s.list[threadIdx.x];
+      int before = 0;                            // pages that go first
+      for (int j = 0; j < num_close; ++j)
+        before += s.list[j] > x || (s.list[j] == x && s.list_page[j] < i);
+      if (before < rest) atomicOr(&words[i / 32], 1u << (i & 31));
+    }
+  } else {
+    // many equal or nearly equal pages: select their exact scores the same way, then the lowest
+    // pages among those equal to the last score that is taken
+    clear_extremes(s);
+    unsigned long long lo = ~0ull, hi = 0ull;
+    for (int j = warp_id(); j < num_close; j += THREADS / 32) {
+      const double e = exact_score<D>(a, b, g, first + near_page[j]);
+      if (lane == 0) near_score[j] = e;
+      const unsigned long long x = order_key(e);
+      lo = x < lo ? x : lo;
+      hi = x > hi ? x : hi;
+    }
+    merge_extremes(s, lo, hi);
     __syncthreads();
     int over;
-    tc = kth_largest<uint64_t>(
-        s, num_close, rest, [&](int i) -> unsigned long long { return order_key(near_score[i]); },
+    const unsigned long long tc = kth_largest(
+        s, num_close, rest, [&](int j) -> unsigned long long { return order_key(near_score[j]); },
         over);
-    ties = rest - over;
-  }
-  // among the close pages equal to tc the first `ties` are taken
-  int equal = 0;
-  if (judge)
-    for (int j = close0; j < close0 + close; ++j) equal += order_key(near_score[j]) == tc;
-  else
-    equal = close;
-  const int equal0 = block_prefix(s, equal);
-  int emit = sure + max(0, min(equal, ties - equal0));
-  if (judge)
-    for (int j = close0; j < close0 + close; ++j) emit += order_key(near_score[j]) > tc;
-  int out = a.sink + block_prefix(s, emit);
-  int j = close0, eq = equal0;
-  for (int i = i0; i < i1; ++i) {
-    const int c = side(i);
-    bool take = c > 0;
-    if (c == 0) {
-      if (judge) {
-        const uint64_t x = order_key(near_score[j]);
-        take = x > tc || (x == tc && eq++ < ties);
-      } else {
-        take = eq++ < ties;
-      }
-      ++j;
+    // pages equal to tc by falling page number; the others count as 0
+    auto tie_key = [&](int j) -> unsigned long long {
+      return order_key(near_score[j]) == tc ? 0xffffffffull - static_cast<uint32_t>(near_page[j])
+                                            : 0ull;
+    };
+    clear_extremes(s);
+    lo = ~0ull;
+    hi = 0ull;
+    for (int j = threadIdx.x; j < num_close; j += THREADS) {
+      const unsigned long long x = tie_key(j);
+      lo = x < lo ? x : lo;
+      hi = x > hi ? x : hi;
     }
-    if (take) sel[out++] = first + i;
+    merge_extremes(s, lo, hi);
+    __syncthreads();
+    int ignore;
+    const unsigned long long edge = kth_largest(s, num_close, rest - over, tie_key, ignore);
+    for (int j = threadIdx.x; j < num_close; j += THREADS) {
+      if (order_key(near_score[j]) > tc || (tie_key(j) != 0 && tie_key(j) >= edge)) {
+        const int i = near_page[j];
+        atomicOr(&words[i / 32], 1u << (i & 31));
+      }
+    }
+  }
+  __syncthreads();
+  int out = a.sink;
+  for (int w0 = 0; w0 < num_words; w0 += THREADS) {
+    const int w = w0 + static_cast<int>(threadIdx.x);
+    uint32_t bits = w < num_words ? words[w] : 0u;
+    int at = out + block_prefix(s, __popc(bits));
+    while (bits != 0) {
+      const int e = __ffs(static_cast<int>(bits)) - 1;
+      bits &= bits - 1;
+      sel[at++] = first + w * 32 + e;
+    }
+    out += s.total;
   }
 }
 
 size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct SparseLayout {
-  size_t decode, score, near_score, near_page, sel, total;
+  size_t head, rows, part_o, part_ml, score, near_score, near_page, words, sel, total;
 };
 SparseLayout sparse_layout(int B, int Hq, int Hkv, int D, int max_blocks, int pages) {
   SparseLayout l;
   const size_t rows = static_cast<size_t>(B) * Hkv;
-  l.decode = 0;
-  l.score = align_up(decode_workspace_bytes(B, Hq, D, pages));
+  const size_t parts = (static_cast<size_t>(B) + stream_max_ranges(Hkv)) * Hq;
+  l.head = 0;
+  l.rows = 256;
+  l.part_o = align_up(l.rows + static_cast<size_t>(B) * sizeof(int4));
+  l.part_ml = align_up(l.part_o + parts * D * sizeof(float));
+  l.score = align_up(l.part_ml + parts * sizeof(float2));
   l.near_score = align_up(l.score + rows * max_blocks * sizeof(float2));
   l.near_page = align_up(l.near_score + rows * max_blocks * sizeof(double));
-  l.sel = align_up(l.near_page + rows * max_blocks * sizeof(int32_t));
+  l.words = align_up(l.near_page + rows * max_blocks * sizeof(int32_t));
+  l.sel = align_up(l.words + rows * ((max_blocks + 31) / 32) * sizeof(uint32_t));
   l.total = align_up(l.sel + rows * pages * sizeof(int32_t));
   return l;
 }
 
 template <int D>
 kara_status launch_sparse_d(const SparseArgs& a, cudaStream_t stream) {
-  if (a.max_blocks > a.pages) {                  // some sequence may have pages to choose from
-    int sms = 148;
-    const int dev = device_slot();
-    if (dev >= 0) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t tiles = static_cast<int64_t>(a.B) * a.Hkv * ((a.max_blocks + 15) / 16);
-    const int64_t most = (tiles + kScoreWarps - 1) / kScoreWarps;
-    const int64_t wave = static_cast<int64_t>(sms) * 2;
-    launch_pdl(page_score_kernel<D>, dim3(static_cast<unsigned>(most < wave ? most : wave)),
-               dim3(kScoreThreads), 0, stream, a);
-  }
-  launch_pdl(page_select_kernel<D>, dim3(static_cast<unsigned>(a.B * a.Hkv)), dim3(kSelThreads),
-             0, stream, a);
+  int sms = 148;
+  const int dev = device_slot();
+  if (dev >= 0) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  // no sequence has pages to choose from when all of them fit: one block writes the line
+  const int64_t tiles = a.max_blocks > a.pages
+                            ? static_cast<int64_t>(a.B) * a.Hkv * ((a.max_blocks + 15) / 16)
+                            : 1;
+  const int64_t most = (tiles + kScoreWarps - 1) / kScoreWarps;
+  const int64_t wave = static_cast<int64_t>(sms) * kScoreBlocks;
+  launch_pdl(page_score_kernel<D>, dim3(static_cast<unsigned>(most < wave ? most : wave)),
+             dim3(kScoreThreads), 0, stream, a);
+  const dim3 rows(static_cast<unsigned>(a.B * a.Hkv));
+  launch_pdl(page_select_kernel<D>, rows, dim3(kSelThreads), 0, stream, a);
   return check_launch("paged_sparse_attn");
 }
 
@@ -474,7 +608,10 @@ kara_status launch_sparse(const SparseLaunch& L, cudaStream_t stream) {
   a.score = reinterpret_cast<float2*>(ws + lay.score);
   a.near_page = reinterpret_cast<int32_t*>(ws + lay.near_page);
   a.near_score = reinterpret_cast<double*>(ws + lay.near_score);
+  a.words = reinterpret_cast<uint32_t*>(ws + lay.words);
   a.sel = L.sel != nullptr ? L.sel : reinterpret_cast<int32_t*>(ws + lay.sel);
+  a.rows = reinterpret_cast<int4*>(ws + lay.rows);
+  a.total = reinterpret_cast<int*>(ws + lay.head);
   a.status = L.status;
   a.B = L.B;
   a.Hq = L.Hq;
@@ -485,28 +622,41 @@ kara_status launch_sparse(const SparseLaunch& L, cudaStream_t stream) {
   a.sink = L.sink;
   a.recent = L.recent;
   a.extra = L.new_slots;
-  const kara_status st = L.D == 128 ? launch_sparse_d<128>(a, stream) : launch_sparse_d<64>(a, stream);
+  kara_status st = L.D == 128 ? launch_sparse_d<128>(a, stream) : launch_sparse_d<64>(a, stream);
   if (st != KARA_OK) return st;
-  DecodeLaunch d;
-  d.q = L.q;
-  d.k_cache = L.k_cache;
-  d.v_cache = L.v_cache;
-  d.block_table = L.block_table;
-  d.ctx_len = L.ctx_len;
-  d.out = L.out;
-  d.partial = reinterpret_cast<float*>(ws + lay.decode);
-  d.status = L.status;
-  d.B = L.B;
-  d.Hq = L.Hq;
-  d.Hkv = L.Hkv;
-  d.D = L.D;
-  d.max_blocks = L.max_blocks;
-  d.num_blocks = L.num_blocks;
-  d.scale = L.scale;
-  d.extra = L.new_slots;
-  d.sel = a.sel;
-  d.sel_pages = L.pages;
-  return launch_decode(d, stream);
+  StreamLaunch t;
+  t.q = L.q;
+  t.k_cache = L.k_cache;
+  t.v_cache = L.v_cache;
+  t.block_table = L.block_table;
+  t.status = L.status;
+  t.sel = a.sel;
+  t.sel_pages = L.pages;
+  t.line.rows = a.rows;
+  t.line.total = a.total;
+  t.line.max_ranges = 0;
+  t.line.min_pages = kListMinPages;
+  t.part_o = reinterpret_cast<float*>(ws + lay.part_o);
+  t.part_ml = reinterpret_cast<float2*>(ws + lay.part_ml);
+  t.B = L.B;
+  t.Hq = L.Hq;
+  t.Hkv = L.Hkv;
+  t.D = L.D;
+  t.max_blocks = L.max_blocks;
+  t.num_blocks = L.num_blocks;
+  t.scale = L.scale;
+  t.beside = false;
+  if ((st = launch_stream(&t, stream)) != KARA_OK) return st;
+  JoinLaunch j = {};
+  j.line = t.line;
+  j.part_o = t.part_o;
+  j.part_ml = t.part_ml;
+  j.out = L.out;
+  j.B = L.B;
+  j.Hq = L.Hq;
+  j.Hkv = L.Hkv;
+  j.D = L.D;
+  return launch_join(j, stream);
 }
 
 }  // namespace kara

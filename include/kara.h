@@ -573,7 +573,7 @@ kara_status lacache_compact(const kara_layer_kv* layers, int32_t num_layers,
  *  KARA_OP_LACACHE: num_seqs, budget in `k_or_budget`.
  *  KARA_OP_SPARSE:  pool's batch, num_kv_heads, head_dim, max_blocks_per_seq; num_q_heads;
  *                   num_pages in `k_or_budget`.
- *  KARA_OP_PREFIX:  pool's batch, head_dim, max_blocks_per_seq; num_q_heads.
+ *  KARA_OP_PREFIX:  pool's batch, num_kv_heads, head_dim; num_q_heads.
  * `pool` is a host pointer (may be NULL for SCORE).
  */
 size_t kara_workspace_bytes(kara_op op, const kara_pool* pool, int32_t num_seqs, int32_t window,

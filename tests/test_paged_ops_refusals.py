@@ -131,9 +131,10 @@ def test_workspace_sizes_hold_the_partials(lib_path):
     def size(op, k=0, **kw):
         return K.lib().kara_workspace_bytes(op, ctypes.byref(pool(**kw)), 0, 0, 4, k)
 
-    assert size(K.OP_SPARSE, 8) >= 3 * 4 * 1 * 130 * 4 + 3 * 2 * 64 * 20 + 3 * 2 * 8 * 4
-    assert size(K.OP_SPARSE, 9) >= 3 * 4 * 2 * 130 * 4
-    assert size(K.OP_PREFIX) >= (3 * 4 + 256 * 148 + 3 * 4 * 8) * 130 * 4
+    ranges = 148 * 3 * 4 // 2                        # warps of the streaming kernel per KV head
+    assert size(K.OP_SPARSE, 8) >= (3 + ranges) * 4 * 130 * 4 + 3 * 2 * 64 * 20 + 3 * 2 * 8 * 4
+    assert size(K.OP_PREFIX) >= (3 * 4 + 256 * 148 + (3 + ranges) * 4) * 130 * 4
+    assert size(K.OP_PREFIX, width=65536) == size(K.OP_PREFIX)
     assert size(K.OP_SPARSE, 0) == 0 and size(K.OP_PREFIX, batch=0) == 0
     big = size(K.OP_SPARSE, 64, batch=4096, width=65536, hkv=8)
     assert big > 2 ** 32 * 8
