@@ -1,5 +1,6 @@
-"""Python binding of libkara (ctypes). Argument marshalling only: every step runs in the CUDA
-library declared in include/kara.h. Torch provides device memory and the current stream.
+"""Python binding of libkara (ctypes; the per-layer calls around the paged cache through the
+extension module _native). Argument marshalling only: every step runs in the CUDA library
+declared in include/kara.h. Torch provides device memory and the current stream.
 
 The functions carry the C names:
     kara_score, kara_select, kara_token2chunk, kara_compact, paged_decode_attn,
@@ -624,84 +625,30 @@ def kara_wait_probe(wait_ms: int, status: torch.Tensor | None = None, device="cu
 
 # ---------------------------------------------------------------------------------------
 # Operators around the paged cache. A decode step makes these calls once per layer, so their
-# checks are written to cost little when they pass: every condition is tested inline and the
-# error text is put together only when one fails.
+# tensors are checked and taken apart by the extension module _native (csrc/native.cpp), which
+# calls the library on the current stream; what it allocates belongs to that stream.
 # ---------------------------------------------------------------------------------------
-def _check_tensor(t, dtype, shape, name: str) -> int:
-    """A contiguous CUDA tensor of this dtype and shape: its address."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
-            and t.is_contiguous()):
-        _require(t, dtype, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+_NATIVE = None
 
 
-def _check_optional(t, dtype, shape, name: str):
-    return None if t is None else _check_tensor(t, dtype, shape, name)
+def _native():
+    """The marshalling module, bound to the loaded library."""
+    global _NATIVE
+    if _NATIVE is None:
+        lib()
+        if not os.path.exists(_build.NATIVE):
+            raise KaraLibraryError(f"{_build.NATIVE} is missing: build it with "
+                                   "`python -m decode_kv_cache_kara_b200.build`")
+        from . import _native as module
+        module.bind(library_path())
+        _NATIVE = module
+    return _NATIVE
 
 
-def _check_heads(t, heads: int, d: int, name: str) -> int:
-    """[tokens, heads, d] bf16 whose rows are contiguous (any stride between tokens): the
-    stride between its tokens."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(shape)}")
-    row, head, one = t.stride()
-    if (one != 1 or (heads > 1 and head != d)) and shape[0]:
-        raise ValueError(f"{name}'s heads must be contiguous within a token")
-    return row if shape[0] > 1 else heads * d
-
-
-def _check_device(stream, tensors) -> int:
-    """Every tensor on the current device, and the stream too: the device's index."""
-    device = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{device}")
-    if stream is not None and stream.device.index != device:
-        raise ValueError(f"the stream is on {stream.device}, the current device is "
-                         f"cuda:{device}")
-    return device
-
-
-def _allocate(stream, fn):
-    """fn() with what it allocates tied to the stream that the call runs on."""
-    if stream is None:
-        return fn()
-    with torch.cuda.stream(stream):
-        return fn()
-
-
-def _raw_stream(stream, device: int) -> int:
-    return (torch._C._cuda_getCurrentRawStream(device) if stream is None
-            else stream.cuda_stream)
-
-
-def _status_ptr(status, stream, device: int):
-    """The status word (a new zeroed one if None) and its address."""
-    if status is None:
-        status = _allocate(stream, lambda: new_status(torch.device("cuda", device)))
-    elif not (isinstance(status, torch.Tensor) and status.is_cuda
-              and status.dtype is torch.int32):
-        _require(status, torch.int32, "status")
-    return status, status.data_ptr()
-
-
-def _workspace_ptr(workspace, nbytes, stream, device: int):
-    """The caller's workspace (its size is checked by the call), or a new one of nbytes()."""
-    if workspace is None:
-        size = max(nbytes(), 256)
-        workspace = _allocate(stream, lambda: torch.empty(
-            size, dtype=torch.uint8, device=torch.device("cuda", device)))
-    elif not (isinstance(workspace, torch.Tensor) and workspace.is_cuda
-              and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
-        _require(workspace, torch.uint8, "workspace")
-    return workspace, workspace.data_ptr(), workspace.numel()
+def _result(out, where: str):
+    if type(out) is int:
+        raise KaraError(out, where)
+    return out
 
 
 def paged_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -715,42 +662,15 @@ def paged_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache
     [T, Hkv, d] (parts of one projection output are fine), inv_freq fp32 [rotary_dim / 2],
     positions int32 [T], cu_tokens int32 [B + 1] (None: one token per sequence). Returns the
     rotated queries [T, Hq, d] (see paged_rope_append in include/kara.h)."""
-    bf16, int32 = torch.bfloat16, torch.int32
-    hkv, d, nb = pool.num_kv_heads, pool.head_dim, pool.num_blocks
-    cache = (nb, pool.page_size, hkv, d)
-    kc = _check_tensor(k_cache, bf16, cache, "k_cache")
-    vc = _check_tensor(v_cache, bf16, cache, "v_cache")
-    batch = pool.block_table.shape[0]
-    tokens, hq = q.shape[:2] if isinstance(q, torch.Tensor) and q.dim() == 3 else (0, 0)
-    qs, ks = _check_heads(q, hq, d, "q"), _check_heads(k, hkv, d, "k")
-    vs = _check_heads(v, hkv, d, "v")
-    if k.shape[0] != tokens or v.shape[0] != tokens:
-        raise ValueError("q, k and v must hold the same tokens")
-    half = inv_freq.numel() if isinstance(inv_freq, torch.Tensor) else 0
-    fp = _check_tensor(inv_freq, torch.float32, (half,), "inv_freq")
-    pp = _check_tensor(positions, int32, (tokens,), "positions")
-    cp = _check_optional(cu_tokens, int32, (batch + 1,), "cu_tokens")
-    if cp is None and tokens != batch:
-        raise ValueError("without cu_tokens there must be one token per sequence")
-    bp = _check_optional(bounds, bf16, (nb, hkv, 2, d), "bounds")
-    rp = _check_optional(q_ring, bf16, (batch, 2 * window, hq, d), "q_ring")
-    ps = pool.c_struct()
-    device = _check_device(stream, (q, k, v, k_cache, v_cache, pool.block_table, pool.ctx_len,
-                                    inv_freq, positions, cu_tokens, bounds, q_ring, q_out, k_out,
-                                    status))
-    if q_out is None:
-        q_out = _allocate(stream, lambda: torch.empty((tokens, hq, d), dtype=bf16,
-                                                      device=q.device))
-    op = _check_tensor(q_out, bf16, (tokens, hq, d), "q_out")
-    kp = _check_optional(k_out, bf16, (tokens, hkv, d), "k_out")
-    status, sp = _status_ptr(status, stream, device)
-    code = lib().paged_rope_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, tokens, cp, pp, fp, 2 * half,
-        1 if interleaved else 0, kc, vc, ps, hq, bp, rp, window, op, kp, sp,
-        _raw_stream(stream, device))
-    if code:
-        raise KaraError(code, "paged_rope_append")
-    return q_out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return paged_rope_append(q, k, v, k_cache, v_cache, pool, inv_freq, positions,
+                                     cu_tokens, interleaved, bounds, q_ring, window, q_out, k_out,
+                                     status)
+    return _result((_NATIVE or _native()).rope_append(
+        q, k, v, k_cache, v_cache, pool.block_table, pool.ctx_len, pool.num_blocks,
+        pool.num_kv_heads, pool.head_dim, pool.page_size, inv_freq, positions, cu_tokens,
+        interleaved, bounds, q_ring, window, q_out, k_out, status), "paged_rope_append")
 
 
 def paged_page_bounds(k_cache: torch.Tensor, pool: PagedPool, bounds: torch.Tensor | None = None,
@@ -759,22 +679,13 @@ def paged_page_bounds(k_cache: torch.Tensor, pool: PagedPool, bounds: torch.Tens
     """Elementwise minimum and maximum of the keys of complete pages: bounds
     [num_blocks, Hkv, 2, d] bf16 (a new one starts at zero), for the pages that hold a slot
     >= from_slot [B] (None: every page)."""
-    bf16 = torch.bfloat16
-    hkv, d, nb = pool.num_kv_heads, pool.head_dim, pool.num_blocks
-    kc = _check_tensor(k_cache, bf16, (nb, pool.page_size, hkv, d), "k_cache")
-    fp = _check_optional(from_slot, torch.int32, (pool.block_table.shape[0],), "from_slot")
-    ps = pool.c_struct()
-    device = _check_device(stream, (k_cache, pool.block_table, pool.ctx_len, bounds, from_slot,
-                                    status))
-    shape = (nb, hkv, 2, d)
-    if bounds is None:
-        bounds = _allocate(stream, lambda: torch.zeros(shape, dtype=bf16, device=k_cache.device))
-    bp = _check_tensor(bounds, bf16, shape, "bounds")
-    status, sp = _status_ptr(status, stream, device)
-    code = lib().paged_page_bounds(kc, ps, fp, new_slots, bp, sp, _raw_stream(stream, device))
-    if code:
-        raise KaraError(code, "paged_page_bounds")
-    return bounds
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return paged_page_bounds(k_cache, pool, bounds, from_slot, new_slots, status)
+    return _result((_NATIVE or _native()).page_bounds(
+        k_cache, pool.block_table, pool.ctx_len, pool.num_blocks, pool.num_kv_heads,
+        pool.head_dim, pool.page_size, bounds, from_slot, new_slots, status),
+        "paged_page_bounds")
 
 
 def paged_sparse_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -785,32 +696,14 @@ def paged_sparse_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                       status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """One decode step over the num_pages pages of each (sequence, KV head) that the page bounds
     select: out [B, Hq, d] bf16; sel [B, Hkv, num_pages] int32, if given, gets the pages."""
-    bf16 = torch.bfloat16
-    hkv, d, nb = pool.num_kv_heads, pool.head_dim, pool.num_blocks
-    cache = (nb, pool.page_size, hkv, d)
-    kc = _check_tensor(k_cache, bf16, cache, "k_cache")
-    vc = _check_tensor(v_cache, bf16, cache, "v_cache")
-    batch = pool.block_table.shape[0]
-    hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
-    qp = _check_tensor(q, bf16, (batch, hq, d), "q")
-    bp = _check_tensor(bounds, bf16, (nb, hkv, 2, d), "bounds")
-    lp = _check_optional(sel, torch.int32, (batch, hkv, num_pages), "sel")
-    ps = pool.c_struct()
-    device = _check_device(stream, (q, k_cache, v_cache, bounds, pool.block_table, pool.ctx_len,
-                                    sel, out, workspace, status))
-    if out is None:
-        out = _allocate(stream, lambda: torch.empty_like(q))
-    op = _check_tensor(out, bf16, (batch, hq, d), "out")
-    status, sp = _status_ptr(status, stream, device)
-    workspace, wp, wn = _workspace_ptr(
-        workspace, lambda: lib().kara_workspace_bytes(OP_SPARSE, ps, 0, 0, hq, num_pages), stream,
-        device)
-    code = lib().paged_sparse_attn(
-        qp, kc, vc, bp, ps, hq, 1.0 / math.sqrt(d) if scale is None else scale, num_pages,
-        sink_pages, recent_pages, new_slots, lp, op, wp, wn, sp, _raw_stream(stream, device))
-    if code:
-        raise KaraError(code, "paged_sparse_attn")
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return paged_sparse_attn(q, k_cache, v_cache, bounds, pool, num_pages, sink_pages,
+                                     recent_pages, new_slots, scale, sel, out, workspace, status)
+    return _result((_NATIVE or _native()).sparse_attn(
+        q, k_cache, v_cache, bounds, pool.block_table, pool.ctx_len, pool.num_blocks,
+        pool.num_kv_heads, pool.head_dim, pool.page_size, num_pages, sink_pages, recent_pages,
+        new_slots, scale, sel, out, workspace, status), "paged_sparse_attn")
 
 
 def paged_prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -822,30 +715,11 @@ def paged_prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     """One decode step for groups of rows that share their first prefix_pages [groups] pages;
     group j is the rows (or entries of group_rows [B]) group_ptr[j] .. group_ptr[j+1] - 1.
     out [B, Hq, d] bf16; rows in no group are not written."""
-    bf16, int32 = torch.bfloat16, torch.int32
-    hkv, d = pool.num_kv_heads, pool.head_dim
-    cache = (pool.num_blocks, pool.page_size, hkv, d)
-    kc = _check_tensor(k_cache, bf16, cache, "k_cache")
-    vc = _check_tensor(v_cache, bf16, cache, "v_cache")
-    batch = pool.block_table.shape[0]
-    hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
-    qp = _check_tensor(q, bf16, (batch, hq, d), "q")
-    groups = prefix_pages.numel() if isinstance(prefix_pages, torch.Tensor) else 0
-    pp = _check_tensor(prefix_pages, int32, (groups,), "prefix_pages")
-    gp = _check_tensor(group_ptr, int32, (groups + 1,), "group_ptr")
-    rp = _check_optional(group_rows, int32, (batch,), "group_rows")
-    ps = pool.c_struct()
-    device = _check_device(stream, (q, k_cache, v_cache, pool.block_table, pool.ctx_len,
-                                    group_ptr, prefix_pages, group_rows, out, workspace, status))
-    if out is None:
-        out = _allocate(stream, lambda: torch.empty_like(q))
-    op = _check_tensor(out, bf16, (batch, hq, d), "out")
-    status, sp = _status_ptr(status, stream, device)
-    workspace, wp, wn = _workspace_ptr(
-        workspace, lambda: lib().kara_workspace_bytes(OP_PREFIX, ps, 0, 0, hq, 0), stream, device)
-    code = lib().paged_prefix_attn(
-        qp, kc, vc, ps, hq, 1.0 / math.sqrt(d) if scale is None else scale, gp, pp, groups, rp,
-        new_slots, op, wp, wn, sp, _raw_stream(stream, device))
-    if code:
-        raise KaraError(code, "paged_prefix_attn")
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return paged_prefix_attn(q, k_cache, v_cache, pool, group_ptr, prefix_pages,
+                                     group_rows, new_slots, scale, out, workspace, status)
+    return _result((_NATIVE or _native()).prefix_attn(
+        q, k_cache, v_cache, pool.block_table, pool.ctx_len, pool.num_blocks,
+        pool.num_kv_heads, pool.head_dim, pool.page_size, group_ptr, prefix_pages, group_rows,
+        new_slots, scale, out, workspace, status), "paged_prefix_attn")
