@@ -28,11 +28,11 @@ namespace {
 
 constexpr int kKeys = 128;              // keys per step
 constexpr int kTilePages = kKeys / 16;
-constexpr int kHalfKeys = 96;           // keys whose weights are handed over first
+constexpr int kPart = 64;               // keys whose weights are handed over first
 constexpr int kRows = 128;              // query rows per tensor-core tile
 static_assert(kItemRows == 2 * kRows, "one tensor-core tile per softmax team");
 constexpr int kMaxCtas = 160;           // grid limit (workspace rows are sized by it)
-constexpr int kMinTiles = 2;            // key tiles that are worth a block of their own
+constexpr int kMinTiles = 1;            // key tiles that are worth a block of their own
 constexpr int kTailMinPages = 4;         // a row's own pages that are worth a warp
 
 struct PrefixArgs {
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     flat += items.start[kPlanThreads];
   }
   if (threadIdx.x == 0) {
-    const long long most = flat / (kMinTiles + kItemCost);
+    const long long most = flat / kMinTiles;
     a.head->total = flat;
     a.head->ctas = static_cast<int>(most < 1 ? 1 : most < a.ctas ? most : a.ctas);
   }
@@ -159,6 +159,23 @@ __device__ __forceinline__ float2 ex2_poly2(float2 x) {
 // Items of up to kRows query rows go to team 0 alone, larger ones half to each team.
 __device__ __forceinline__ int team0_rows(int rows) { return rows > kRows ? (rows + 1) / 2 : rows; }
 
+// Warp-wide wait: every lane calls it and gets the same answer. Bounded (about 1.6 s at boost
+// clock) and short: the hot loops have to stay in the instruction cache (with 82 KB of code one
+// fetch in twenty missed it and tiles took twice as long). A wait that gives up raises *abort,
+// which the block reports when it leaves.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint32_t t0 = static_cast<uint32_t>(clock());
+#pragma unroll 1
+    do {
+      ok = mbar_try_wait(bar, parity);
+    } while (!ok && *abort == 0 && static_cast<uint32_t>(clock()) - t0 < 3000000000u);
+    if (!ok) *abort = 1;
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
 // The part of an item that one block works on: key tiles [kt0, kt1).
 struct Seg {
   int first, row0, pages, g, kt0, kt1, q0, rows;   // q0: first query row of the item in its group
@@ -214,7 +231,8 @@ struct SegCursor {
   }
 };
 
-constexpr int kPfxThreads = 384;        // warp 0: TMA, warp 1: UMMA, warps 4-11: softmax teams
+constexpr int kPfxThreads = 384;        // warp 0: TMA, warps 1-2: UMMA, warps 4-11: softmax teams
+constexpr int kTeamThreads = 128;       // one thread per query row
 constexpr int kRegsLow = 72, kRegsHigh = 208;   // registers a thread after the split
 constexpr uint32_t kTmemS = 0;          // S of team w at 128 w; its P (bf16) over S's columns
 constexpr uint32_t kTmemO = 256;        // O of team w at 256 + 128 w
@@ -228,7 +246,7 @@ struct PfxSmem {
   static constexpr uint32_t q_off = 0;
   static constexpr uint32_t kv_off = 2 * kTile;
   static constexpr uint32_t bar_off = kv_off + kStages * kTile;
-  static constexpr int kBars = 2 * kStages + 2 + 3 + 2 + 2 + 2 + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 3 + 4 + 2 + 2 + 8;
   static constexpr uint32_t bytes = bar_off + kBars * 8 + 16;
 };
 
@@ -248,28 +266,30 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   uint64_t* kv_empty = kv_full + kStages;
   uint64_t* q_full = kv_empty + kStages;      // [2] the team's queries are in shared memory
   uint64_t* s_full = q_full + 2;              // [3] S of team w; [2]: team 0's second buffer
-  uint64_t* p_half = s_full + 3;              // [2] P of the first keys, S read, O rescaled
-  uint64_t* p_full = p_half + 2;              // [2] all of P
-  uint64_t* o_full = p_full + 2;              // [2] O += P V done
+  uint64_t* p_full = s_full + 3;              // [team][part]: P written, S read, O rescaled
+  uint64_t* o_full = p_full + 4;              // [2] O += P V done
   uint64_t* drained = o_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  uint64_t* turn = drained + 2;               // [team][quad]: the warp may exponentiate
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);               // one arrival per issuer
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&q_full[w], 4);
+      mbar_init(&q_full[w], kTeamThreads / 32);
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_half[w], 4);
-      mbar_init(&p_full[w], 4);
+      mbar_init(&p_full[2 * w], 4);
+      mbar_init(&p_full[2 * w + 1], 4);
       mbar_init(&o_full[w], 1);
     }
     mbar_init(&s_full[2], 1);
-    mbar_init(drained, 1);
+    mbar_init(&drained[0], 1);
+    mbar_init(&drained[1], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&turn[i], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -290,8 +310,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   cur.init(a, blockIdx.x);
   Seg sg;
 
-  // registers: four warps give up what the eight softmax warps take; the launch has checked that
-  // the block was given that many
+  // registers: four warps give up what the softmax warps take; the launch has checked that the
+  // block was given that many
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");   // kRegsLow
   if (warp == 0) {
     // ---- TMA producer: K(0), then K(i), V(i - 1), the order of use ----
@@ -301,13 +321,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     int issued = 0;
     bool ok = true;
-    const int page = lane / NCH, ch = lane % NCH;
+    const bool elected = elect_one();
     while (ok && cur.next(a, sg)) {
       const int32_t* table = a.block_table + static_cast<size_t>(sg.row0) * a.max_blocks;
       // pages past the prefix in its last tile: its last page again (their weights are 0)
       auto block_of = [&](int kt) -> int {
-        if (lane >= kTilePages * NCH) return 0;
-        int blk = table[min(kt * kTilePages + page, sg.pages - 1)];
+        if (lane >= kTilePages) return 0;
+        int blk = table[min(kt * kTilePages + lane, sg.pages - 1)];
         if (blk < 0 || blk >= a.num_blocks) {
           report(a.status, KARA_ERR_BAD_BLOCK);
           blk = 0;
@@ -316,23 +336,31 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       };
       auto load = [&](const CUtensorMap* tm, int blk) -> bool {
         const int st = issued % kStages;
-        int go = 1;
-        if (lane == 0) {
-          go = mbar_wait(&kv_empty[st], ((issued / kStages) & 1) ^ 1, abort_flag, a.status) ? 1 : 0;
-          if (go) mbar_expect_tx(&kv_full[st], L::kTile);
+        if (!wait_warp(&kv_empty[st], ((issued / kStages) & 1) ^ 1, abort_flag))
+          return false;
+        if (elected) mbar_expect_tx(&kv_full[st], L::kTile);
+#pragma unroll
+        for (int p = 0; p < kTilePages; ++p) {
+          const int id = __shfl_sync(0xffffffffu, blk, p);
+          if (elected) {
+#pragma unroll
+            for (int ch = 0; ch < NCH; ++ch)
+              tma_load_4d(kv_buf + st * L::kTile + ch * L::kChunk + p * 2048, tm, &kv_full[st],
+                          ch * 64, sg.g, 0, id);
+          }
         }
-        if (!__shfl_sync(0xffffffffu, go, 0)) return false;
-        if (lane < kTilePages * NCH)
-          tma_load_4d(kv_buf + st * L::kTile + ch * L::kChunk + page * 2048, tm, &kv_full[st],
-                      ch * 64, sg.g, 0, blk);
+        __syncwarp();
         ++issued;
         return true;
       };
       int blk = block_of(sg.kt0), blk_v = 0;
       for (int kt = sg.kt0; ok && kt <= sg.kt1; ++kt) {
         const int blk_next = kt + 1 < sg.kt1 ? block_of(kt + 1) : 0;
-        if (kt < sg.kt1) ok = load(&tm_k, blk);
-        if (ok && kt > sg.kt0) ok = load(&tm_v, blk_v);
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+          const bool key = e == 0;
+          if (ok && (key ? kt < sg.kt1 : kt > sg.kt0)) ok = load(key ? &tm_k : &tm_v, key ? blk : blk_v);
+        }
         blk_v = blk;
         blk = blk_next;
       }
@@ -342,86 +370,100 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       volatile int give_up = 0;
       for (int st = 0; st < kStages; ++st)
         if (issued > st)
-          mbar_wait(&kv_full[st], ((issued - 1 - st) / kStages) & 1, &give_up, a.status);
+          wait_warp(&kv_full[st], ((issued - 1 - st) / kStages) & 1, &give_up);
     }
-  } else if (warp == 1) {
-    // ---- UMMA issuer. Two teams: per step i and team w, O_w += P_w(i-1) V(i-1), then S_w(i) =
-    // Q_w K(i)^T, so that one team's products run while the other team exponentiates; S_w(i)
-    // overwrites P_w(i-1). One team: S(i) goes to the buffers in turn, ahead of O += P(i-1)
-    // V(i-1), so that the team's next tile is ready when it has finished one. Products execute
-    // in issue order. ----
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D) | (1u << 16);   // V is N-major
-      uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
-      int used = 0;                             // ring entries consumed
-      bool ok = true;
-      while (ok && cur.next(a, sg)) {
-        const int teams = sg.rows > kRows ? 2 : 1;
-        const int n = sg.kt1 - sg.kt0;
-        for (int w = 0; ok && w < teams; ++w) {
-          ok = mbar_wait(&q_full[w], q_ph[w], abort_flag, a.status);
-          q_ph[w] ^= 1;
-        }
-        for (int i = 0; ok && i <= n; ++i) {
-          const int k_at = used, v_at = used + (i < n ? 1 : 0);
-          const int ks = k_at % kStages, vs = v_at % kStages;
-          auto scores = [&](int w, int buf) {   // S = Q_w K(i)^T into buffer buf
-            tc_fence_after();
-            const uint32_t q_addr = smem_u32(q_buf + w * L::kTile);
-            const uint32_t k_addr = smem_u32(kv_buf + ks * L::kTile);
+  } else if (warp == 1 || warp == 2) {
+    // ---- UMMA issuers, one per team. Step i of team w: O_w += P_w(i-1) V(i-1), then S_w(i) = Q_w
+    // K(i)^T, which overwrites P_w(i-1) (a thread's products execute in the order of issue). The
+    // teams' steps interleave: one team's products, and its issuer's waits (about 100 cycles
+    // each, as long as two products), run while the other team exponentiates. One team alone:
+    // S(i) goes to the buffers in turn, ahead of O += P(i-1) V(i-1), so that the team's next
+    // tile is ready when it has finished one. The warp waits, an elected thread issues. ----
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D) | (1u << 16);   // V is N-major
+    const int w = warp - 1;
+    const bool elected = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return wait_warp(bar, parity, abort_flag);
+    };
+    uint32_t q_ph = 0, p_ph = 0;
+    int used = 0;                               // ring entries consumed
+    bool ok = true;
+    while (ok && cur.next(a, sg)) {
+      const bool both = sg.rows > kRows;
+      const bool on = w == 0 || both;
+      const int n = sg.kt1 - sg.kt0;
+      if (on) {
+        ok = wait(&q_full[w], q_ph);
+        q_ph ^= 1;
+      }
+      for (int i = 0; ok && i <= n; ++i) {
+        const int k_at = used, v_at = used + (i < n ? 1 : 0);
+        const int ks = k_at % kStages, vs = v_at % kStages;
+        auto scores = [&]() -> bool {           // S = Q_w K(i)^T
+          if (!wait(&kv_full[ks], (k_at / kStages) & 1)) return false;
+          tc_fence_after();
+          if (elected) {
+            if (on) {
+              const int buf = both ? w : i & 1;
+              const uint32_t q_addr = smem_u32(q_buf + w * L::kTile);
+              const uint32_t k_addr = smem_u32(kv_buf + ks * L::kTile);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * L::kChunk + (k & 3) * 32;
-              umma_bf16(tmem + kTmemS + buf * 128, sw128_kmajor_desc(q_addr + off),
-                        sw128_kmajor_desc(k_addr + off), idesc_s, k > 0 ? 1u : 0u);
-            }
-          };
-          auto weigh = [&](int w, int buf) -> bool {   // O_w += P(i-1) V(i-1)
-            if (!mbar_wait(&kv_full[vs], (v_at / kStages) & 1, abort_flag, a.status)) return false;
-            const uint32_t v_addr = smem_u32(kv_buf + vs * L::kTile);
-            for (int part = 0; part < 2; ++part) {
-              if (!mbar_wait(part == 0 ? &p_half[w] : &p_full[w], p_ph[w], abort_flag, a.status))
-                return false;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k) {
-                if ((k < kHalfKeys / 16) != (part == 0)) continue;
-                umma_bf16_ts(tmem + kTmemO + w * 128, tmem + kTmemS + buf * 128 + k * 8,
-                             sw128_mnmajor_desc(v_addr + k * 2048, L::kChunk, 1024), idesc_o,
-                             (i > 1 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * L::kChunk + (k & 3) * 32;
+                umma_bf16(tmem + kTmemS + buf * 128, sw128_kmajor_desc(q_addr + off),
+                          sw128_kmajor_desc(k_addr + off), idesc_s, k > 0 ? 1u : 0u);
               }
+              umma_commit(&s_full[both ? w : (i & 1) * 2]);
             }
-            p_ph[w] ^= 1;
-            umma_commit(&o_full[w]);
-            return true;
-          };
-          if (i < n) ok = mbar_wait(&kv_full[ks], (k_at / kStages) & 1, abort_flag, a.status);
-          if (ok && teams == 1) {
-            if (i < n) {
-              scores(0, i & 1);
-              umma_commit(&s_full[(i & 1) * 2]);
-            }
-            if (i > 0) ok = weigh(0, (i - 1) & 1);
-          } else {
-            for (int w = 0; ok && w < 2; ++w) {
-              if (i > 0) ok = weigh(w, w);
-              if (ok && i < n) {
-                scores(w, w);
-                umma_commit(&s_full[w]);
-              }
-            }
+            umma_commit(&kv_empty[ks]);
           }
-          if (ok && i > 0) umma_commit(&kv_empty[vs]);
-          if (ok && i < n) umma_commit(&kv_empty[ks]);
-          used += (i < n ? 1 : 0) + (i > 0 ? 1 : 0);
+          __syncwarp();
+          return true;
+        };
+        auto weigh = [&]() -> bool {            // O_w += P(i-1) V(i-1)
+          if (!wait(&kv_full[vs], (v_at / kStages) & 1)) return false;
+          if (on) {
+            const int buf = both ? w : (i - 1) & 1;
+            const uint32_t v_addr = smem_u32(kv_buf + vs * L::kTile);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              if (!wait(&p_full[2 * w + part], p_ph)) return false;
+              tc_fence_after();
+              if (elected) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k) {
+                  if ((k < kPart / 16) != (part == 0)) continue;
+                  umma_bf16_ts(tmem + kTmemO + w * 128, tmem + kTmemS + buf * 128 + k * 8,
+                               sw128_mnmajor_desc(v_addr + k * 2048, L::kChunk, 1024), idesc_o,
+                               (i > 1 || k > 0) ? 1u : 0u);
+                }
+                if (part == 1) umma_commit(&o_full[w]);
+              }
+              __syncwarp();
+            }
+            p_ph ^= 1;
+          }
+          if (elected) umma_commit(&kv_empty[vs]);
+          __syncwarp();
+          return true;
+        };
+#pragma unroll 1
+        for (int e = 0; ok && e < 2; ++e) {
+          if ((e == 0) != both) {
+            if (i < n) ok = scores();
+          } else {
+            if (i > 0) ok = weigh();
+          }
         }
+        used += (i < n ? 1 : 0) + (i > 0 ? 1 : 0);
       }
-      if (!ok) {                                // products in flight still read shared memory
-        volatile int give_up = 0;
-        umma_commit(drained);
-        mbar_wait(drained, 0, &give_up, a.status);
-      }
+    }
+    if (!ok) {                                  // products in flight still read shared memory
+      volatile int give_up = 0;
+      if (elected) umma_commit(&drained[w]);
+      __syncwarp();
+      wait_warp(&drained[w], 0, &give_up);
     }
   } else if (warp >= 4) {
     // ---- softmax teams: a thread owns one query row (TMEM lane) and holds its 128 scores of a
@@ -436,19 +478,20 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t flip = a.negate ? 0x80008000u : 0u;
     const float2 cs2 = make_float2(a.cs, a.cs);
     uint32_t s_ph[3] = {0, 0, 0}, o_ph = 0;   // o_ph: parity of the next product to complete
+    uint32_t t_ph = w == 0 ? 1 : 0;           // team 0 goes first
     bool aborted = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool ok = aborted ? false : mbar_wait(bar, parity, abort_flag, a.status);
-      aborted = __any_sync(0xffffffffu, !ok) != 0;
+      if (!aborted) aborted = !wait_warp(bar, parity, abort_flag);
     };
     while (!aborted && cur.next(a, sg)) {
-      const int half = team0_rows(sg.rows);
-      const int row0 = w == 0 ? 0 : half;       // the team's rows of the item
-      const int live = w == 0 ? half : sg.rows - half;
+      const int rows0 = team0_rows(sg.rows);
+      const int row0 = w == 0 ? 0 : rows0;      // the team's rows of the item
+      const int live = w == 0 ? rows0 : sg.rows - rows0;
       if (live <= 0) continue;
       const bool one_team = sg.rows <= kRows;
       const bool warp_on = quad * 32 < live;
-      // the warp's 32 query rows into the swizzled tile, 16 bytes per lane, whole rows at a time
+      // the warp's 32 query rows into the swizzled tile, 16 bytes per lane, all in flight at once
+      // (rows past the last: copies of it, whose results are not read)
       if (warp_on) {
         constexpr int kPer = D / 8;             // lanes per row
         constexpr int kTurns = kPer;            // 32 rows, 32 / kPer at a time
@@ -488,60 +531,78 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         wait(&s_full[bar], s_ph[bar]);
         s_ph[bar] ^= 1;
         if (aborted) break;
-        bool waited = i == 0;                   // for O += P V of step i - 1
-        if (warp_on) {
+        if (!warp_on) {
+          // not before product i - 1: an arrival for step i must not count for the step before
+          if (i > 0) {
+            wait(&o_full[w], o_ph);
+            o_ph ^= 1;
+          }
+          if (!one_team) {
+            wait(&turn[w * 4 + quad], t_ph);
+            t_ph ^= 1;
+          }
+          if (lane == 0) {
+            if (!one_team) mbar_arrive(&turn[(w ^ 1) * 4 + quad]);
+            mbar_arrive(&p_full[2 * w]);
+            mbar_arrive(&p_full[2 * w + 1]);
+          }
+        } else {
           tc_fence_after();
           const uint32_t s_col = lane_base + kTmemS + buf * 128;
-          // a chunk's loads are in flight while the chunk before it goes into the row maximum
-          float v[kKeys];
           const int valid = (sg.pages - (sg.kt0 + i) * kTilePages) * 16;
+          if (valid < kKeys) {                  // pages past the prefix: their scores become -inf
+#pragma unroll 1
+            for (int c = valid; c < kKeys; c += 16) tmem_st16_fill(s_col + c, -INFINITY);
+            tmem_wait_st();
+          }
+          float v[kKeys];
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_col + c, v + c);
+          tmem_wait_ld();
+          reg_fence<kKeys>(v);
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          tmem_ld32(s_col, v);
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
-            tmem_wait_ld();
-            reg_fence<32>(v + c);
-            if (c + 32 < kKeys) tmem_ld32(s_col + c + 32, v + c + 32);
-            if (valid < kKeys) {
+          for (int e = 0; e < kKeys; e += 8) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[c + e] = c + e < valid ? v[c + e] : -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-#pragma unroll
-              for (int t = 0; t < 4; ++t) mq[t] = fmax3(mq[t], v[c + e + 2 * t], v[c + e + 2 * t + 1]);
-            }
+            for (int t = 0; t < 4; ++t) mq[t] = fmax3(mq[t], v[e + 2 * t], v[e + 2 * t + 1]);
           }
           const float mx = fmaxf(fmax3(mq[0], mq[1], mq[2]), mq[3]);
           // the base moves only when the row maximum outgrows it by 2^8 (or on the first tile):
           // weights up to 2^8 lose nothing in fp32 sums and floating bf16
           const bool move = i > 0 && (mx - m) * a.cs > 8.f;
           if (i == 0) m = mx;
+          bool waited = i == 0;                 // for O += P V of step i - 1
           if (__any_sync(0xffffffffu, move)) {
-            if (!waited) wait(&o_full[w], o_ph);   // O is complete up to step i - 1
+            wait(&o_full[w], o_ph);             // O is complete up to step i - 1
             waited = true;
-            if (!aborted) {
-              tc_fence_after();
-              const float to = move ? mx : m;
-              const float f = to == m ? 1.f : ex2((m - to) * a.cs);
-              m = to;
-              l *= f;
+            if (aborted) break;
+            tc_fence_after();
+            const float to = move ? mx : m;
+            const float f = to == m ? 1.f : ex2((m - to) * a.cs);
+            m = to;
+            l *= f;
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                float o[16];
-                uint32_t u[16];
-                tmem_ld16(o_col + c, o);
-                tmem_wait_ld();
-                reg_fence<16>(o);
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              uint32_t u[16];
+              tmem_ld16(o_col + c, o);
+              tmem_wait_ld();
+              reg_fence<16>(o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
-                tmem_st16(o_col + c, u);
-              }
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
+              tmem_st16(o_col + c, u);
             }
           }
           // m - m: a base of +inf makes the whole row NaN, as it should be
           const float nb = m == -INFINITY ? 0.f : (m - m) - m * a.cs;
           const float2 nb2 = make_float2(nb, nb);
+          // the two teams' warps of a scheduler exponentiate in turns: left to themselves they fall
+          // into step, share the exponential unit and then both wait for their products
+          if (!one_team) {
+            wait(&turn[w * 4 + quad], t_ph);
+            t_ph ^= 1;
+            if (aborted) break;
+          }
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < kKeys; c += 32) {
@@ -554,26 +615,26 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
               const __nv_bfloat162 pb = __floats2bfloat162_rn(p.x, p.y);
               u[e / 2] = *reinterpret_cast<const uint32_t*>(&pb);
             }
-            if (c == kHalfKeys) {               // the product may start on the first keys
+            tmem_st16(s_col + c / 2, u);
+            if (c == kPart - 32) {              // the product may start on the first keys
+              if (!waited) wait(&o_full[w], o_ph);   // its phase: none is ever two behind
+              waited = true;
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&p_half[w]);
+              if (lane == 0) mbar_arrive(&p_full[2 * w]);
             }
-            tmem_st16(s_col + c / 2, u);
           }
           sum[0] = fadd2(sum[0], sum[1]);
           l += sum[0].x + sum[0].y;
+          if (!one_team && lane == 0) mbar_arrive(&turn[(w ^ 1) * 4 + quad]);
           tmem_wait_st();
           tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * w + 1]);
+          if (i > 0) o_ph ^= 1;
+          if (aborted) break;
         }
-        // every product's phase is waited for, so that none is ever two behind
-        if (!waited) wait(&o_full[w], o_ph);
-        if (!warp_on && lane == 0) mbar_arrive(&p_half[w]);
-        if (i > 0) o_ph ^= 1;
-        if (aborted) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w]);
       }
       if (aborted) break;
       wait(&o_full[w], o_ph);
@@ -604,6 +665,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag != 0) report(a.status, KARA_ERR_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -649,7 +711,7 @@ kara_status launch_prefix_d(const PrefixArgs& a, const CUtensorMap& tk, const CU
     cudaFuncAttributes attr;
     if (cudaFuncGetAttributes(&attr, prefix_attn_kernel<D>) != cudaSuccess)
       return check_launch("paged_prefix_attn");
-    if (attr.numRegs * kPfxThreads < 128 * kRegsLow + 256 * kRegsHigh) {
+    if (attr.numRegs * kPfxThreads < 128 * kRegsLow + 2 * kTeamThreads * kRegsHigh) {
       set_last_error("paged_prefix_attn", "the kernel was built with too few registers");
       return KARA_ERR_CUDA;
     }

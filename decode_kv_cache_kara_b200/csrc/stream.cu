@@ -130,6 +130,7 @@ page_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int R = stream_ranges(a.line, total);
   // neighbouring warps take the KV heads of the same pages, whose rows lie side by side in HBM
   const long long jobs = static_cast<long long>(R) * a.Hkv;
+  const bool elected = elect_one();
   int issued = 0, done = 0;
   uint32_t phase = 0;      // parity bit per stage
   uint32_t pending = 0;    // stages with a load issued and not yet consumed
@@ -191,13 +192,15 @@ page_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int blk = __shfl_sync(0xffffffffu, in_cu ? ids_cu : ids_nu, j & 31);
         const int st = issued % kStages;
         if (blk >= 0) pending |= 1u << st;
-        if (lane == 0 && blk >= 0) {
+        if (elected && blk >= 0) {
           uint8_t* dst = my_ring + st * kPage;
           mbar_expect_tx(&my_bars[st], kPage);
           const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+#pragma unroll
           for (int c = 0; c < NCH; ++c)
             tma_load_4d(dst + c * kChunkBytes, tm, &my_bars[st], c * 64, g, 0, blk);
         }
+        __syncwarp();
         ++issued;
       }
     };
