@@ -33,7 +33,7 @@ constexpr int kRows = 128;              // query rows per tensor-core tile
 static_assert(kItemRows == 2 * kRows, "one tensor-core tile per softmax team");
 constexpr int kMaxCtas = 160;           // grid limit (workspace rows are sized by it)
 constexpr int kMinTiles = 1;            // key tiles that are worth a block of their own
-constexpr int kTailMinPages = 4;         // a row's own pages that are worth a warp
+constexpr int kTailMinPages = 2;         // a row's own pages that are worth a warp
 
 struct PrefixArgs {
   const __nv_bfloat16* q;

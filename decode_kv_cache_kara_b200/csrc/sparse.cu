@@ -139,26 +139,28 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) page_score_kernel
       for (int c = 0; c < NC; ++c) {
         const uint4 qv = grp < G ? qrow[c * 4 + tig] : zero;
         const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w};
-        uint32_t neg[4], pos[4], mag[4];
+        uint32_t neg[4], pos[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const __nv_bfloat162 t = *reinterpret_cast<const __nv_bfloat162*>(&qw[j]);
           const __nv_bfloat162 m = __hmin2(t, none), p = __hmax2(t, none);
           neg[j] = *reinterpret_cast<const uint32_t*>(&m);
           pos[j] = *reinterpret_cast<const uint32_t*>(&p);
-          mag[j] = qw[j] & 0x7fff7fffu;
         }
         const uint4 l0 = x0[c], l1 = x1[c], h0 = x0[NC + c], h1 = x1[NC + c];
-        mma_bf16_16816(s, l0.x, l1.x, l0.y, l1.y, neg[0], neg[1]);
-        mma_bf16_16816(s, l0.z, l1.z, l0.w, l1.w, neg[2], neg[3]);
-        mma_bf16_16816(s, h0.x, h1.x, h0.y, h1.y, pos[0], pos[1]);
-        mma_bf16_16816(s, h0.z, h1.z, h0.w, h1.w, pos[2], pos[3]);
-        // |q| (|lo| + |hi|) >= the terms' magnitudes
+        // four steps (64 terms) from zero: their errors stay those of 64 terms
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
         const uint32_t k = 0x7fff7fffu;
-        mma_bf16_16816(e, l0.x & k, l1.x & k, l0.y & k, l1.y & k, mag[0], mag[1]);
-        mma_bf16_16816(e, l0.z & k, l1.z & k, l0.w & k, l1.w & k, mag[2], mag[3]);
-        mma_bf16_16816(e, h0.x & k, h1.x & k, h0.y & k, h1.y & k, mag[0], mag[1]);
-        mma_bf16_16816(e, h0.z & k, h1.z & k, h0.w & k, h1.w & k, mag[2], mag[3]);
+        mma_bf16_16816(t, l0.x, l1.x, l0.y, l1.y, neg[0], neg[1]);
+        mma_bf16_16816(e, l0.x & k, l1.x & k, l0.y & k, l1.y & k, neg[0] & k, neg[1] & k);
+        mma_bf16_16816(t, l0.z, l1.z, l0.w, l1.w, neg[2], neg[3]);
+        mma_bf16_16816(e, l0.z & k, l1.z & k, l0.w & k, l1.w & k, neg[2] & k, neg[3] & k);
+        mma_bf16_16816(t, h0.x, h1.x, h0.y, h1.y, pos[0], pos[1]);
+        mma_bf16_16816(e, h0.x & k, h1.x & k, h0.y & k, h1.y & k, pos[0] & k, pos[1] & k);
+        mma_bf16_16816(t, h0.z, h1.z, h0.w, h1.w, pos[2], pos[3]);
+        mma_bf16_16816(e, h0.z & k, h1.z & k, h0.w & k, h1.w & k, pos[2] & k, pos[3] & k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += t[i];
       }
       // rows grp and grp + 8, heads 2 tig and 2 tig + 1: the maximum over the group's heads
       const bool h0 = 2 * tig < G, h1 = 2 * tig + 1 < G;
@@ -194,7 +196,8 @@ __device__ __forceinline__ uint64_t order_key(double x) {
 }
 
 constexpr int kListMinPages = 2;                 // selected pages that are worth a warp
-constexpr int kSelBits = 11;
+constexpr int kSelBits = 10;
+constexpr int kSelFew = 64;                      // scores that are ranked by counting
 constexpr int kSelBins = 1 << kSelBits;
 constexpr int kSelList = 512;                    // candidates settled by counting
 constexpr int kSelWords = 2048;                  // pages in the shared bitmap, / 32
@@ -207,6 +210,7 @@ struct SelectSmem {
   uint32_t words[kSelWords];
   int warp_total[THREADS / 32];
   unsigned long long lo, hi;     // extreme keys
+  uint32_t key_lo, key_hi;
   unsigned long long found;
   int bin, above, in_bin, total, count, sure, close;
   float err;
@@ -256,7 +260,7 @@ __device__ unsigned long long kth_largest(SelectSmem<THREADS>& s, int n, int k, 
     for (int i = threadIdx.x; i < kSelBins; i += THREADS) s.hist[i] = 0;
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-#pragma unroll 4
+#pragma unroll 8
     for (int i = threadIdx.x; i < n; i += THREADS) {
       const unsigned long long x = key(i);
       if ((shift < 64 ? x >> shift : 0ull) == prefix)
@@ -288,7 +292,7 @@ __device__ unsigned long long kth_largest(SelectSmem<THREADS>& s, int n, int k, 
     shift = next;
     const int in_bin = s.in_bin;
     if (shift > 0 && in_bin <= min(kSelList, THREADS)) {
-#pragma unroll 4
+#pragma unroll 8
       for (int i = threadIdx.x; i < n; i += THREADS) {
         const unsigned long long x = key(i);
         if (x >> shift == prefix) s.list[atomicAdd(&s.count, 1)] = x;
@@ -343,39 +347,56 @@ __device__ __forceinline__ void clear_extremes(SelectSmem<THREADS>& s) {
   __syncthreads();
 }
 
-// Error of an fp32 score, relative to the sum of its terms' magnitudes: 2 d <= 256 terms enter
-// 16 tensor-core steps; each step adds 17 numbers whose alignment may drop bits below 2^-23 of
-// the largest, at most 16 * 17 * 2^-23 = 2^-14.9 in all, and the magnitudes themselves are
-// computed as (|lo| + |hi|) |q| >= them with the same relative error.
-constexpr float kScoreErr = 1.0f / 16384.0f;
+// Error of an fp32 score, relative to the sum of its terms' magnitudes (e). A tensor-core step
+// adds 16 exact products to the sum so far and drops bits below 2^-23 of the largest of the 17
+// numbers, at most 17 * 2^-23 of it; over the four steps of a chain that is at most 68 * 2^-23 of
+// the chain's e, over all chains 2^-16.9 e. The fp32 additions of the at most 4 chains are off by
+// 2^-24 of partial sums below e each. e itself is summed in one chain, low by at most 2^-14 of
+// its value. (Measured worst 2^-20.)
+constexpr float kScoreErr = 1.0f / 65536.0f;
 
-// The largest of the group's exact scores of one page (a warp's work, every lane gets it).
+// The largest of the group's exact scores of one page (a warp's work, every lane gets it). Four
+// lanes per query head, each with every fourth 8-channel piece.
 template <int D>
 __device__ __forceinline__ double exact_score(const SparseArgs& a, int b, int g, int page) {
   const int G = a.Hq / a.Hkv;
   const int blk = a.block_table[static_cast<size_t>(b) * a.max_blocks + page];
-  double best = -INFINITY;
-  if (blk < 0 || blk >= a.num_blocks) return best;
-  const __nv_bfloat16* lo = a.bounds + (static_cast<size_t>(blk) * a.Hkv + g) * 2 * D;
-  const __nv_bfloat16* q0 = a.q + (static_cast<size_t>(b) * a.Hq + g * G) * D;
-  float l[D / 32], u[D / 32];
+  if (blk < 0 || blk >= a.num_blocks) return -INFINITY;
+  const int h = lane_id() >> 2, part = lane_id() & 3;
+  const uint4* lo = reinterpret_cast<const uint4*>(
+      a.bounds + (static_cast<size_t>(blk) * a.Hkv + g) * 2 * D);
+  const uint4* qr = reinterpret_cast<const uint4*>(
+      a.q + (static_cast<size_t>(b) * a.Hq + g * G + min(h, G - 1)) * D);
+  uint4 l[D / 32], u[D / 32], x[D / 32];
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
-    l[c] = __bfloat162float(lo[c * 32 + lane_id()]);
-    u[c] = __bfloat162float(lo[D + c * 32 + lane_id()]);
+    l[c] = lo[c * 4 + part];
+    u[c] = lo[D / 8 + c * 4 + part];
+    x[c] = qr[c * 4 + part];
   }
-#pragma unroll 4
-  for (int h = 0; h < G; ++h) {
-    double sum = 0.0;
+  double sum[2] = {0.0, 0.0};
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      const float x = __bfloat162float(q0[h * D + c * 32 + lane_id()]);
-      // a product of two bf16 numbers is exact in fp64 (and in fp32)
-      sum += static_cast<double>(x) * static_cast<double>(x < 0.f ? l[c] : u[c]);
+  for (int c = 0; c < D / 32; ++c) {
+    const uint32_t* lw = reinterpret_cast<const uint32_t*>(&l[c]);
+    const uint32_t* uw = reinterpret_cast<const uint32_t*>(&u[c]);
+    const uint32_t* xw = reinterpret_cast<const uint32_t*>(&x[c]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      auto up = [](uint32_t w) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
+      const float2 q = up(xw[j]), p = up(lw[j]), r = up(uw[j]);
+      // a product of two bf16 numbers is exact in fp32
+      sum[0] += static_cast<double>(q.x * (q.x < 0.f ? p.x : r.x));
+      sum[1] += static_cast<double>(q.y * (q.y < 0.f ? p.y : r.y));
     }
+  }
+  double best = sum[0] + sum[1];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    best = sum > best ? sum : best;
+  for (int off = 1; off < 4; off <<= 1) best += __shfl_xor_sync(0xffffffffu, best, off);
+  if (h >= G || best != best) best = -INFINITY;
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    const double other = __shfl_xor_sync(0xffffffffu, best, off);
+    best = other > best ? other : best;
   }
   return best;
 }
@@ -419,48 +440,139 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
                         ? s.words
                         : a.words + static_cast<size_t>(bg) * ((a.max_blocks + 31) / 32);
 
-  // extreme scores and the largest error scale
+  // this thread's scores: page threadIdx.x + THREADS j; those past kKept are read again
+  constexpr int kKept = 8;
+  float kept[kKept];
+  const int rounds = (n + THREADS - 1) / THREADS;
   if (threadIdx.x == 0) {
     s.err = 0.f;
-    s.sure = s.close = 0;
+    s.sure = s.close = s.count = 0;
+    s.key_lo = 0xffffffffu;
+    s.key_hi = 0u;
   }
-  clear_extremes(s);
+  for (int i = threadIdx.x; i < kSelBins; i += THREADS) s.hist[i] = 0;
+  float err = 0.f;
+  uint32_t klo = 0xffffffffu, khi = 0u;
+  auto see = [&](float2 x) {
+    const uint32_t k = order_key(x.x);
+    klo = min(klo, k);
+    khi = max(khi, k);
+    err = x.y == x.y ? fmaxf(err, x.y) : INFINITY;
+  };
   {
-    float err = 0.f;
-    unsigned long long lo = ~0ull, hi = 0ull;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += THREADS) {
-      const float2 x = score[i];
-      const unsigned long long u = order_key(x.x);
-      lo = u < lo ? u : lo;
-      hi = u > hi ? u : hi;
-      err = x.y == x.y ? fmaxf(err, x.y) : INFINITY;
-    }
-    merge_extremes(s, lo, hi);
+    float2 x[kKept];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-      err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, off));
-    if (lane == 0) atomicMax(reinterpret_cast<int*>(&s.err), __float_as_int(err));
+    for (int j = 0; j < kKept; ++j) {
+      const int i = threadIdx.x + j * THREADS;
+      x[j] = i < n ? score[i] : make_float2(0.f, 0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < kKept; ++j) {
+      kept[j] = x[j].x;
+      if (static_cast<int>(threadIdx.x) + j * THREADS < n) see(x[j]);
+    }
+  }
+  for (int i = threadIdx.x + kKept * THREADS; i < n; i += THREADS) see(score[i]);
+  // f(page, score) for this thread's pages
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int j = 0; j < kKept; ++j) {
+      const int i = threadIdx.x + j * THREADS;
+      if (i < n) f(i, kept[j]);
+    }
+    for (int i = threadIdx.x + kKept * THREADS; i < n; i += THREADS) f(i, score[i].x);
+  };
+  klo = __reduce_min_sync(0xffffffffu, klo);
+  khi = __reduce_max_sync(0xffffffffu, khi);
+  // magnitudes are not negative: they order as their bits
+  const uint32_t eb = __reduce_max_sync(0xffffffffu, __float_as_uint(err));
+  __syncthreads();
+  if (lane == 0) {
+    atomicMin(&s.key_lo, klo);
+    atomicMax(&s.key_hi, khi);
+    atomicMax(reinterpret_cast<unsigned int*>(&s.err), eb);
   }
   __syncthreads();
-  int above;
-  const uint32_t tkey = static_cast<uint32_t>(kth_largest(
-      s, n, want, [&](int i) -> unsigned long long { return order_key(score[i].x); }, above));
+
+  // The want-th largest fp32 score: radix selection from the highest bit in which the scores
+  // differ (they share sign and most exponent bits, so the first digit already spreads them),
+  // until a bin holds few, which one warp ranks. The scans are a warp's too.
+  uint32_t tkey;
+  {
+    const uint32_t differ = s.key_lo ^ s.key_hi;
+    int shift = 32 - __clz(differ);              // bits to settle
+    uint32_t prefix = shift < 32 ? s.key_hi >> shift : 0u;
+    int rest = want;
+    while (shift > 0) {
+      const int bits = min(kSelBits, shift), next = shift - bits;
+      each([&](int, float x) {
+        const uint32_t k = order_key(x);
+        if ((shift < 32 ? k >> shift : 0u) == prefix)
+          atomicAdd(&s.hist[(k >> next) & ((1u << bits) - 1)], 1);
+      });
+      __syncthreads();
+      if (threadIdx.x < 32) {                    // bins from the top, kSelBins / 32 per lane
+        constexpr int kPer = kSelBins / 32;
+        int sum = 0;
+#pragma unroll 8
+        for (int j = 0; j < kPer; ++j) sum += s.hist[kSelBins - 1 - (lane * kPer + j)];
+        int upto = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += y;
+        }
+        int run = upto - sum;
+        if (run < rest && upto >= rest) {
+          int bin = kSelBins - 1 - lane * kPer;
+          while (run + s.hist[bin] < rest) run += s.hist[bin--];
+          s.bin = bin;
+          s.above = run;
+          s.in_bin = s.hist[bin];
+        }
+      }
+      __syncthreads();
+      prefix = (prefix << bits) | static_cast<uint32_t>(s.bin);
+      rest -= s.above;
+      shift = next;
+      if (shift == 0) break;
+      const int in_bin = s.in_bin;
+      if (in_bin <= kSelFew) {
+        uint32_t* list = reinterpret_cast<uint32_t*>(s.list);
+        each([&](int, float x) {
+          const uint32_t k = order_key(x);
+          if (k >> shift == prefix) list[atomicAdd(&s.count, 1)] = k;
+        });
+        __syncthreads();
+        for (int j0 = threadIdx.x; j0 < in_bin; j0 += THREADS) {
+          const uint32_t mine = list[j0];
+          int more = 0, same = 0;
+          for (int j = 0; j < in_bin; ++j) {
+            more += list[j] > mine;
+            same += list[j] == mine;
+          }
+          if (more < rest && more + same >= rest) s.found = mine;   // equal keys: equal values
+        }
+        __syncthreads();
+        prefix = static_cast<uint32_t>(s.found);
+        shift = 0;
+      } else {
+        for (int i = threadIdx.x; i < kSelBins; i += THREADS) s.hist[i] = 0;
+        __syncthreads();
+      }
+    }
+    tkey = prefix;
+  }
   const float t = tkey == 0u ? __int_as_float(0x7fc00000)
                              : __uint_as_float((tkey & 0x80000000u) ? tkey ^ 0x80000000u : ~tkey);
   const float margin = 2.f * kScoreErr * s.err;
   // every page: surely among the best, surely not, or near the border
-  for (int i0 = threadIdx.x - lane; i0 < num_words * 32; i0 += THREADS) {
-    const int i = i0 + lane;
-    bool sure = false, close = false;
-    if (i < n) {
-      const float x = score[i].x;
-      sure = x > t + margin;
-      close = !sure && !(x < t - margin);
-    }
+  auto judge = [&](int i, float x) {
+    const bool sure = i < n && x > t + margin;
+    const bool close = i < n && !sure && !(x < t - margin);
     const uint32_t ws = __ballot_sync(0xffffffffu, sure), wc = __ballot_sync(0xffffffffu, close);
-    if (lane == 0) {
-      words[i0 / 32] = ws;
+    if (lane == 0 && i < num_words * 32) {
+      words[i / 32] = ws;
       if (ws != 0) atomicAdd(&s.sure, __popc(ws));
     }
     if (wc != 0) {
@@ -469,15 +581,24 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
       at = __shfl_sync(0xffffffffu, at, 0) + __popc(wc & ((1u << lane) - 1));
       if (close) {
         if (at < kSelList) s.list_page[at] = i;
-        near_page[at] = i;
+        else near_page[at] = i;
       }
     }
+  };
+#pragma unroll
+  for (int j = 0; j < kKept; ++j)
+    if (j < rounds) judge(threadIdx.x + j * THREADS, kept[j]);
+  for (int j = kKept; j < rounds; ++j) {
+    const int i = threadIdx.x + j * THREADS;
+    judge(i, i < n ? score[i].x : 0.f);
   }
   __syncthreads();
   const int num_close = s.close, rest = want - s.sure;   // places left for the close pages
+  // the close pages: the first kSelList in shared memory, the rest in the workspace
+  auto close_page = [&](int j) -> int { return j < kSelList ? s.list_page[j] : near_page[j]; };
   if (rest >= num_close) {                       // all of them
     for (int j = threadIdx.x; j < num_close; j += THREADS) {
-      const int i = near_page[j];
+      const int i = close_page(j);
       atomicOr(&words[i / 32], 1u << (i & 31));
     }
   } else if (num_close <= min(kSelList, THREADS)) {
@@ -500,7 +621,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
     clear_extremes(s);
     unsigned long long lo = ~0ull, hi = 0ull;
     for (int j = warp_id(); j < num_close; j += THREADS / 32) {
-      const double e = exact_score<D>(a, b, g, first + near_page[j]);
+      const double e = exact_score<D>(a, b, g, first + close_page(j));
       if (lane == 0) near_score[j] = e;
       const unsigned long long x = order_key(e);
       lo = x < lo ? x : lo;
@@ -514,7 +635,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
         over);
     // pages equal to tc by falling page number; the others count as 0
     auto tie_key = [&](int j) -> unsigned long long {
-      return order_key(near_score[j]) == tc ? 0xffffffffull - static_cast<uint32_t>(near_page[j])
+      return order_key(near_score[j]) == tc ? 0xffffffffull - static_cast<uint32_t>(close_page(j))
                                             : 0ull;
     };
     clear_extremes(s);
@@ -531,23 +652,33 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
     const unsigned long long edge = kth_largest(s, num_close, rest - over, tie_key, ignore);
     for (int j = threadIdx.x; j < num_close; j += THREADS) {
       if (order_key(near_score[j]) > tc || (tie_key(j) != 0 && tie_key(j) >= edge)) {
-        const int i = near_page[j];
+        const int i = close_page(j);
         atomicOr(&words[i / 32], 1u << (i & 31));
       }
     }
   }
   __syncthreads();
-  int out = a.sink;
-  for (int w0 = 0; w0 < num_words; w0 += THREADS) {
-    const int w = w0 + static_cast<int>(threadIdx.x);
-    uint32_t bits = w < num_words ? words[w] : 0u;
-    int at = out + block_prefix(s, __popc(bits));
-    while (bits != 0) {
-      const int e = __ffs(static_cast<int>(bits)) - 1;
-      bits &= bits - 1;
-      sel[at++] = first + w * 32 + e;
+  // out in ascending order: one warp numbers the words' pages, every thread writes its own
+  int* start = num_words <= kSelBins ? s.hist : near_page;   // the counts are no longer needed
+  if (threadIdx.x < 32) {
+    int carry = a.sink;
+    for (int w0 = 0; w0 < num_words; w0 += 32) {
+      const int w = w0 + lane;
+      const int mine = w < num_words ? __popc(words[w]) : 0;
+      int upto = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += y;
+      }
+      if (w < num_words) start[w] = carry + upto - mine;
+      carry += __shfl_sync(0xffffffffu, upto, 31);
     }
-    out += s.total;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += THREADS) {
+    const uint32_t bits = words[i / 32], bit = 1u << (i & 31);
+    if (bits & bit) sel[start[i / 32] + __popc(bits & (bit - 1))] = first + i;
   }
 }
 
