@@ -197,10 +197,13 @@ __device__ __forceinline__ uint64_t order_key(double x) {
 
 constexpr int kListMinPages = 2;                 // selected pages that are worth a warp
 constexpr int kSelBits = 10;
+constexpr int kSelKeys = 4096;                   // pages whose keys stay in shared memory
+constexpr int kDigit = 8;                        // bits of a score that one pass settles
+constexpr int kDigitBins = 1 << kDigit;
 constexpr int kSelFew = 64;                      // scores that are ranked by counting
 constexpr int kSelBins = 1 << kSelBits;
 constexpr int kSelList = 512;                    // candidates settled by counting
-constexpr int kSelWords = 2048;                  // pages in the shared bitmap, / 32
+constexpr int kSelWords = 1024;                  // pages in the shared bitmap, / 32
 
 template <int THREADS>
 struct SelectSmem {
@@ -208,6 +211,7 @@ struct SelectSmem {
   unsigned long long list[kSelList];
   int list_page[kSelList];
   uint32_t words[kSelWords];
+  uint32_t keys[kSelKeys];
   int warp_total[THREADS / 32];
   unsigned long long lo, hi;     // extreme keys
   uint32_t key_lo, key_hi;
@@ -440,48 +444,31 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
                         ? s.words
                         : a.words + static_cast<size_t>(bg) * ((a.max_blocks + 31) / 32);
 
-  // this thread's scores: page threadIdx.x + THREADS j; those past kKept are read again
-  constexpr int kKept = 8;
-  float kept[kKept];
-  const int rounds = (n + THREADS - 1) / THREADS;
+  // The row's scores as ordered keys, in shared memory where they fit. This kernel runs its code
+  // once per block, so what it costs most is fetching it: little is unrolled.
+  uint32_t* keys = n <= kSelKeys ? s.keys : reinterpret_cast<uint32_t*>(near_score);
   if (threadIdx.x == 0) {
     s.err = 0.f;
     s.sure = s.close = s.count = 0;
     s.key_lo = 0xffffffffu;
     s.key_hi = 0u;
   }
-  for (int i = threadIdx.x; i < kSelBins; i += THREADS) s.hist[i] = 0;
+  // counts of a digit's values; a word of padding every 8 keeps a warp's scan free of conflicts
+  auto slot = [](uint32_t bin) -> uint32_t { return bin + (bin >> 3); };
+  constexpr int kSlots = kDigitBins + kDigitBins / 8;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < kSlots; i += THREADS) s.hist[i] = 0;
   float err = 0.f;
   uint32_t klo = 0xffffffffu, khi = 0u;
-  auto see = [&](float2 x) {
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += THREADS) {
+    const float2 x = score[i];
     const uint32_t k = order_key(x.x);
+    keys[i] = k;
     klo = min(klo, k);
     khi = max(khi, k);
     err = x.y == x.y ? fmaxf(err, x.y) : INFINITY;
-  };
-  {
-    float2 x[kKept];
-#pragma unroll
-    for (int j = 0; j < kKept; ++j) {
-      const int i = threadIdx.x + j * THREADS;
-      x[j] = i < n ? score[i] : make_float2(0.f, 0.f);
-    }
-#pragma unroll
-    for (int j = 0; j < kKept; ++j) {
-      kept[j] = x[j].x;
-      if (static_cast<int>(threadIdx.x) + j * THREADS < n) see(x[j]);
-    }
   }
-  for (int i = threadIdx.x + kKept * THREADS; i < n; i += THREADS) see(score[i]);
-  // f(page, score) for this thread's pages
-  auto each = [&](auto&& f) {
-#pragma unroll
-    for (int j = 0; j < kKept; ++j) {
-      const int i = threadIdx.x + j * THREADS;
-      if (i < n) f(i, kept[j]);
-    }
-    for (int i = threadIdx.x + kKept * THREADS; i < n; i += THREADS) f(i, score[i].x);
-  };
   klo = __reduce_min_sync(0xffffffffu, klo);
   khi = __reduce_max_sync(0xffffffffu, khi);
   // magnitudes are not negative: they order as their bits
@@ -504,18 +491,21 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
     uint32_t prefix = shift < 32 ? s.key_hi >> shift : 0u;
     int rest = want;
     while (shift > 0) {
-      const int bits = min(kSelBits, shift), next = shift - bits;
-      each([&](int, float x) {
-        const uint32_t k = order_key(x);
+      const int bits = min(kDigit, shift), next = shift - bits;
+#pragma unroll 4
+      for (int i = threadIdx.x; i < n; i += THREADS) {
+        const uint32_t k = keys[i];
         if ((shift < 32 ? k >> shift : 0u) == prefix)
-          atomicAdd(&s.hist[(k >> next) & ((1u << bits) - 1)], 1);
-      });
+          atomicAdd(&s.hist[slot((k >> next) & ((1u << bits) - 1))], 1);
+      }
       __syncthreads();
-      if (threadIdx.x < 32) {                    // bins from the top, kSelBins / 32 per lane
-        constexpr int kPer = kSelBins / 32;
-        int sum = 0;
-#pragma unroll 8
-        for (int j = 0; j < kPer; ++j) sum += s.hist[kSelBins - 1 - (lane * kPer + j)];
+      if (threadIdx.x < 32) {                    // values from the top, eight per lane
+        int c[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          c[j] = s.hist[slot(kDigitBins - 1 - (lane * 8 + j))];
+          sum += c[j];
+        }
         int upto = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -523,12 +513,14 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
           if (lane >= off) upto += y;
         }
         int run = upto - sum;
-        if (run < rest && upto >= rest) {
-          int bin = kSelBins - 1 - lane * kPer;
-          while (run + s.hist[bin] < rest) run += s.hist[bin--];
-          s.bin = bin;
-          s.above = run;
-          s.in_bin = s.hist[bin];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (run < rest && run + c[j] >= rest) {
+            s.bin = kDigitBins - 1 - (lane * 8 + j);
+            s.above = run;
+            s.in_bin = c[j];
+          }
+          run += c[j];
         }
       }
       __syncthreads();
@@ -539,10 +531,9 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
       const int in_bin = s.in_bin;
       if (in_bin <= kSelFew) {
         uint32_t* list = reinterpret_cast<uint32_t*>(s.list);
-        each([&](int, float x) {
-          const uint32_t k = order_key(x);
-          if (k >> shift == prefix) list[atomicAdd(&s.count, 1)] = k;
-        });
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += THREADS)
+          if (keys[i] >> shift == prefix) list[atomicAdd(&s.count, 1)] = keys[i];
         __syncthreads();
         for (int j0 = threadIdx.x; j0 < in_bin; j0 += THREADS) {
           const uint32_t mine = list[j0];
@@ -557,7 +548,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
         prefix = static_cast<uint32_t>(s.found);
         shift = 0;
       } else {
-        for (int i = threadIdx.x; i < kSelBins; i += THREADS) s.hist[i] = 0;
+        for (int i = threadIdx.x; i < kSlots; i += THREADS) s.hist[i] = 0;
         __syncthreads();
       }
     }
@@ -566,13 +557,20 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
   const float t = tkey == 0u ? __int_as_float(0x7fc00000)
                              : __uint_as_float((tkey & 0x80000000u) ? tkey ^ 0x80000000u : ~tkey);
   const float margin = 2.f * kScoreErr * s.err;
-  // every page: surely among the best, surely not, or near the border
-  auto judge = [&](int i, float x) {
-    const bool sure = i < n && x > t + margin;
-    const bool close = i < n && !sure && !(x < t - margin);
+  // every page: surely among the best (a key above that of t + margin), surely not (below that of
+  // t - margin), or near the border; a NaN among them leaves everything near
+  const bool nan = !(t + margin == t + margin) || !(t - margin == t - margin);
+  const uint32_t key_up = nan ? 0xffffffffu : order_key(t + margin);
+  const uint32_t key_low = nan ? 0u : order_key(t - margin);
+#pragma unroll 1
+  for (int i0 = threadIdx.x - lane; i0 < num_words * 32; i0 += THREADS) {
+    const int i = i0 + lane;
+    const uint32_t k = i < n ? keys[i] : 0u;
+    const bool sure = i < n && k > key_up;
+    const bool close = i < n && !sure && k >= key_low;
     const uint32_t ws = __ballot_sync(0xffffffffu, sure), wc = __ballot_sync(0xffffffffu, close);
-    if (lane == 0 && i < num_words * 32) {
-      words[i / 32] = ws;
+    if (lane == 0) {
+      words[i0 / 32] = ws;
       if (ws != 0) atomicAdd(&s.sure, __popc(ws));
     }
     if (wc != 0) {
@@ -584,13 +582,6 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
         else near_page[at] = i;
       }
     }
-  };
-#pragma unroll
-  for (int j = 0; j < kKept; ++j)
-    if (j < rounds) judge(threadIdx.x + j * THREADS, kept[j]);
-  for (int j = kKept; j < rounds; ++j) {
-    const int i = threadIdx.x + j * THREADS;
-    judge(i, i < n ? score[i].x : 0.f);
   }
   __syncthreads();
   const int num_close = s.close, rest = want - s.sure;   // places left for the close pages
@@ -676,6 +667,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
     }
   }
   __syncthreads();
+#pragma unroll 4
   for (int i = threadIdx.x; i < n; i += THREADS) {
     const uint32_t bits = words[i / 32], bit = 1u << (i & 31);
     if (bits & bit) sel[start[i / 32] + __popc(bits & (bit - 1))] = first + i;
