@@ -23,7 +23,7 @@ namespace kara {
 namespace {
 
 constexpr int kAppThreads = 256;
-constexpr int kAppBatch = 4;       // heads a thread has in flight
+constexpr int kAppBatch = 6;       // heads a thread has in flight
 
 struct AppendArgs {
   const __nv_bfloat16* q;
@@ -86,7 +86,7 @@ __device__ __forceinline__ void page_bounds_unit(const __nv_bfloat16* k_cache,
 // A thread owns 16 channels of one token (two 16-byte vectors that hold 8 rotation pairs),
 // whose sines it needs for every head, and walks the heads: queries, keys, then values.
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kAppThreads) rope_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppThreads, 2) rope_append_kernel(const AppendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int U = D / 16;                      // 16-channel units per head
