@@ -565,3 +565,173 @@ def test_on_another_stream_and_captured():
     replayed = [t.clone() for t in out]
     for a, b in zip(replayed, step()):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------- far ends and odd callers
+
+@pytest.mark.parametrize("kind", ["random", "equal", "two_values"])
+@pytest.mark.parametrize("pages", [4500, 33000])
+def test_sparse_selection_over_many_pages(pages, kind):
+    """More pages than the selection keeps in shared memory, and hundreds of equal scores."""
+    d, keep = 64, 700
+    n = pages * PAGE - 7
+    gen = torch.Generator().manual_seed(71)
+    c = Cache(71, [16, n], 1, d)
+    if kind == "equal":
+        c.k[:] = c.k[0:1]
+    elif kind == "two_values":
+        c.k[:] = torch.where(torch.rand(c.num_blocks, 1, 1, 1, generator=gen) < 0.5, 1.0, -1.0)
+    c.kd = c.k.cuda()
+    q = bf16(gen, 2, 3, d)
+    bounds = c.bounds()
+    sel = torch.empty((2, 1, keep), dtype=torch.int32, device="cuda")
+    status = K.new_status()
+    out = K.paged_sparse_attn(q.cuda(), c.kd, c.vd, bounds.cuda(), c.pool, keep, sel=sel,
+                              status=status)
+    assert K.read_status(status) == 0
+    for b, m in enumerate(c.lengths):
+        s = op.page_scores(H.f64(q[b]), H.f64(bounds), c.table[b, :-(-int(m) // PAGE)])
+        assert np.array_equal(H.i32(sel[b, 0]), op.select_pages(s[0], keep, 1, 2))
+    ref, mag = op.sparse_attention(H.f64(q), c.k.float().numpy(), c.v.float().numpy(),
+                                   H.i32(sel), c.table, c.lengths, 0.125, PAGE)
+    attention_close(out, ref, mag)
+
+
+def test_blocks_behind_32_bit_offsets():
+    """The same sequences in blocks far up a pool of more than 2^31 elements: bit for bit what
+    they give in a small pool."""
+    hkv, d, hq, far = 8, 128, 16, 140_000
+    c, ptr = prefix_cache(72, [3, 2], [5, 2], hkv, d)
+    i = dict(dtype=torch.int32, device="cuda")
+    big = far + c.num_blocks
+    assert far * PAGE * hkv * d > 2 ** 31
+    kd = torch.empty((big, PAGE, hkv, d), dtype=torch.bfloat16, device="cuda")
+    vd = torch.empty_like(kd)
+    kd[far:], vd[far:] = c.kd, c.vd
+    pool = K.PagedPool(torch.tensor(np.where(c.table >= 0, c.table + far, -1), **i),
+                       c.pool.ctx_len, torch.zeros(big, **i), c.pool.free_top, big, hkv, d)
+    x = bf16(c.gen, 5, hq + 2 * hkv, d).cuda()
+    args = (inv_freq(d).cuda(), i32(np.arange(5) * 1000))
+    results = []
+    for k, v, p in ((c.kd, c.vd, c.pool), (kd, vd, pool)):
+        status = K.new_status()
+        bounds = K.paged_page_bounds(k, p, status=status)
+        q = K.paged_rope_append(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], k, v, p, *args,
+                                bounds=bounds, status=status)
+        results.append((q, K.paged_sparse_attn(q, k, v, bounds, p, 4, new_slots=1, status=status),
+                        K.paged_prefix_attn(q, k, v, p, i32(ptr), i32([5, 2]), new_slots=1,
+                                            status=status),
+                        bounds[-c.num_blocks:], k[-c.num_blocks:], v[-c.num_blocks:]))
+        assert K.read_status(status) == 0
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_prefix_rows_outside_the_groups_and_empty_groups():
+    c, _ = prefix_cache(73, [2, 3], [4, 6], 2, 64)
+    q = bf16(c.gen, 5, 4, 64)
+    for ptr in ([0, 0, 0], [5, 5, 5], [2, 2, 5], [2, 5, 5]):
+        pages = [4, 6] if ptr[1] == ptr[0] else [6, 4]
+        out = torch.full((5, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+        status = K.new_status()
+        K.paged_prefix_attn(q.cuda(), c.kd, c.vd, c.pool, i32(ptr), i32(pages), out=out,
+                            status=status)
+        assert K.read_status(status) == 0
+        rows = np.arange(ptr[0], ptr[2])
+        if len(rows):
+            ref, mag = op.dense_attention(H.f64(q), H.f64(c.k), H.f64(c.v), c.table, c.lengths,
+                                          0.125, PAGE)
+            attention_close(out[rows], ref[rows], mag[rows])
+        rest = [r for r in range(5) if r not in rows]
+        assert (out[rest] == 3).all()
+
+
+def test_nan_in_a_key_reaches_its_rows_only():
+    """A NaN key inside the prefix makes the outputs of its group and KV head NaN, a NaN among a
+    row's own keys those of the row; the others keep their values."""
+    c, ptr = prefix_cache(74, [3, 3], [6, 6], 2, 128, least=20)
+    q = bf16(c.gen, 6, 4, 128)
+    good = check_prefix(c, q, ptr, [6, 6])
+    c.kd[int(c.table[0, 3]), 5, 0] = float("nan")           # group 0, KV head 0
+    c.kd[int(c.table[4, 6]), 1, 1] = float("nan")           # row 4's first own page, KV head 1
+    got = K.paged_prefix_attn(q.cuda(), c.kd, c.vd, c.pool, i32(ptr), i32([6, 6]))
+    bad = torch.zeros((6, 4), dtype=torch.bool, device="cuda")
+    bad[:3, :2] = True
+    bad[4, 2:] = True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], good[~bad])
+
+
+def test_two_calls_at_once_and_no_room():
+    """Calls on two streams at the same time, each with what it allocates itself."""
+    c, ptr = prefix_cache(75, [40, 30], [60, 30], 2, 128, least=3)
+    q = [bf16(c.gen, 70, 8, 128).cuda() for _ in range(2)]
+    bounds = c.bounds().cuda()
+    gp, pp = i32(ptr), i32([60, 30])
+    want = [(K.paged_prefix_attn(x, c.kd, c.vd, c.pool, gp, pp),
+             K.paged_sparse_attn(x, c.kd, c.vd, bounds, c.pool, 12)) for x in q]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(8):
+        for s in range(2):
+            got[s].append((K.paged_prefix_attn(q[s], c.kd, c.vd, c.pool, gp, pp, stream=streams[s]),
+                           K.paged_sparse_attn(q[s], c.kd, c.vd, bounds, c.pool, 12,
+                                               stream=streams[s])))
+    torch.cuda.synchronize()
+    for s in range(2):
+        for pair in got[s]:
+            assert torch.equal(pair[0], want[s][0]) and torch.equal(pair[1], want[s][1])
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for call in (lambda: K.paged_prefix_attn(q[0], c.kd, c.vd, c.pool, gp, pp, workspace=small),
+                 lambda: K.paged_sparse_attn(q[0], c.kd, c.vd, bounds, c.pool, 12,
+                                             workspace=small)):
+        with pytest.raises(K.KaraError, match="workspace"):
+            call()
+
+
+def test_binding_refuses_tensors_that_do_not_fit():
+    c = Cache(76, [20, 40], 2, 64, room=4)
+    x = bf16(c.gen, 2, 8, 64).cuda()
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    freq, pos = inv_freq(64).cuda(), i32([1, 2])
+    bounds = c.bounds().cuda()
+    qc = q.contiguous()
+    gp, pp = i32([0, 2]), i32([1])
+
+    def append(**kw):
+        a = dict(q=q, k=k, v=v, k_cache=c.kd, v_cache=c.vd, pool=c.pool, inv_freq=freq,
+                 positions=pos)
+        a.update(kw)
+        return K.paged_rope_append(**a)
+
+    def sparse(**kw):
+        a = dict(q=qc, k_cache=c.kd, v_cache=c.vd, bounds=bounds, pool=c.pool, num_pages=4)
+        a.update(kw)
+        return K.paged_sparse_attn(**a)
+
+    def prefix(**kw):
+        a = dict(q=qc, k_cache=c.kd, v_cache=c.vd, pool=c.pool, group_ptr=gp, prefix_pages=pp)
+        a.update(kw)
+        return K.paged_prefix_attn(**a)
+
+    wide = torch.zeros((2, 4, 128), dtype=torch.bfloat16, device="cuda")[..., :64]
+    for call, bad in (
+            (append, dict(q=wide)), (append, dict(q=q.float())), (append, dict(k=k[:1])),
+            (append, dict(positions=pos[:1])), (append, dict(positions=pos.long())),
+            (append, dict(inv_freq=freq[::2])), (append, dict(cu_tokens=i32([0, 1]))),
+            (append, dict(k_cache=c.kd[:-1])), (append, dict(v_cache=c.vd.transpose(1, 2))),
+            (append, dict(q_out=qc[:1])), (append, dict(bounds=bounds[:, :1])),
+            (append, dict(q_ring=bounds, window=4)), (append, dict(status=pos.long())),
+            (append, dict(q=q.cpu())), (append, dict(window=2 ** 40)),
+            (sparse, dict(q=q)), (sparse, dict(sel=i32([1]))), (sparse, dict(out=qc[:1])),
+            (sparse, dict(bounds=bounds.float())), (sparse, dict(workspace=pos)),
+            (prefix, dict(group_ptr=i32([0, 1, 2]))), (prefix, dict(group_rows=i32([0]))),
+            (prefix, dict(prefix_pages=pp.long())), (prefix, dict(q=qc.cpu()))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    for call, bad in ((append, dict(inv_freq=freq[:4].contiguous())), (sparse, dict(num_pages=2)),
+                      (sparse, dict(scale=-1.0)), (prefix, dict(new_slots=-1))):
+        with pytest.raises(K.KaraError):
+            call(**bad)
+    given = torch.empty_like(qc)
+    assert sparse(out=given) is given and prefix(out=given) is given
