@@ -11,7 +11,9 @@
 // a compression a slot's number is no longer its token's position.
 //
 // Both kernels move every byte once: HBM-bound for prompts and caches, launch latency for a
-// decode step.
+// decode step. Measured: 15K prompt tokens of 28 + 2 * 4 heads 49.5 us, 4.8 TB/s (72 % of measured;
+// the sines cost 4 us, the bounds 1 us), one token 3.7 us, 128 tokens 4.3 us; bounds of 580K slots
+// 119 us, 6.2 TB/s (94 %).
 #include <cstdint>
 
 #include "common.cuh"
@@ -23,7 +25,10 @@ namespace kara {
 namespace {
 
 constexpr int kAppThreads = 256;
-constexpr int kAppBatch = 6;       // heads a thread has in flight
+// Heads a thread has in flight: 192 bytes of loads (4 heads were 6 % slower on prompts; three
+// blocks per SM with 2 or 3 heads 1 to 6 %; blocks that share an item's heads 30 %, for they
+// repeat its sines and look-ups).
+constexpr int kAppBatch = 6;
 
 struct AppendArgs {
   const __nv_bfloat16* q;

@@ -22,12 +22,18 @@ __device__ __forceinline__ int stream_ranges(const StreamLine& s, int total) {
   const int most = total / s.min_pages;
   return total == 0 ? 0 : most < 1 ? 1 : most < s.max_ranges ? most : s.max_ranges;
 }
+// n / d for n >= 0, d > 0: the 64-bit division only where n needs it.
+__device__ __forceinline__ long long divide(long long n, int d) {
+  return (n >> 32) == 0
+             ? static_cast<long long>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d))
+             : n / d;
+}
 // First page of range r of R on a line of `total` pages, and the range that holds page p.
 __device__ __forceinline__ int range_start(int r, int R, int total) {
-  return static_cast<int>(static_cast<long long>(r) * total / R);
+  return static_cast<int>(divide(static_cast<long long>(r) * total, R));
 }
 __device__ __forceinline__ int range_of(int p, int R, int total) {
-  return static_cast<int>(((static_cast<long long>(p) + 1) * R - 1) / total);
+  return static_cast<int>(divide((static_cast<long long>(p) + 1) * R - 1, total));
 }
 
 // Shared prefixes: the work of all items (group, query tile, KV head) is one line of key tiles,

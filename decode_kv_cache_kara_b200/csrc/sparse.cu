@@ -12,7 +12,9 @@
 //           best of the rest. The set is exactly that of the scores in 64 bits (ties to the
 //           lower page): fp32 scores with a bound on their error decide all pages but those
 //           near the border, and those are scored again in fp64.
-//   attend  the streaming decode kernel over the chosen pages, and its combine.
+//   attend  the streaming kernel over the chosen pages, and its join (stream.cu).
+// 128 sequences of 2K to 16K slots, 28 query and 4 KV heads, 128 pages each: score 30 us (147 MB,
+// 75 % of measured HBM), select 17 us, attend 97 us, join about 6 us.
 #include <cstdint>
 
 #include "common.cuh"
@@ -407,8 +409,9 @@ __device__ __forceinline__ double exact_score(const SparseArgs& a, int b, int g,
 
 // One block per (sequence, KV head). The chosen pages are a bitmap, so that they come out in
 // ascending order from any order of work.
-// 512 threads: rows of 4K pages (few blocks, long passes) took 8 us less than with 256, 512 rows of
-// 600 pages the same.
+// What bounds it is latency: about 15 dependent steps (a load, a barrier, a first fetch of code
+// each), 5 us for a row of 250 pages. 512 threads: a row of 4K pages takes 5 us less than with 256,
+// 512 rows of 600 pages 1 us more; with 1024 threads 2 us less and 10 us more.
 constexpr int kSelThreads = 512;
 
 template <int D>

