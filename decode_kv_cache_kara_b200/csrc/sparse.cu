@@ -410,13 +410,11 @@ __device__ __forceinline__ double exact_score(const SparseArgs& a, int b, int g,
 // One block per (sequence, KV head). The chosen pages are a bitmap, so that they come out in
 // ascending order from any order of work.
 // What bounds it is latency: about 15 dependent steps (a load, a barrier, a first fetch of code
-// each), 5 us for a row of 250 pages. 512 threads: a row of 4K pages takes 5 us less than with 256,
-// 512 rows of 600 pages 1 us more; with 1024 threads 2 us less and 10 us more.
-constexpr int kSelThreads = 512;
-
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseArgs a) {
-  constexpr int THREADS = kSelThreads;
+// each), 5 us for a row of 250 pages. 1024 threads where every block has an SM to itself and rows
+// can be long (one sequence of 4K pages 31.8 -> 30.0 us), else 512 (512 rows of 600 pages 154 us
+// against 164 with 1024 and 153 with 256; 32 sequences of 257 pages 38.6 against 38.9 and 38.2).
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) page_select_kernel(const SparseArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ SelectSmem<THREADS> s;
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SparseAr
   const bool nan = !(t + margin == t + margin) || !(t - margin == t - margin);
   const uint32_t key_up = nan ? 0xffffffffu : order_key(t + margin);
   const uint32_t key_low = nan ? 0u : order_key(t - margin);
-#pragma unroll 1
+#pragma unroll 2
   for (int i0 = threadIdx.x - lane; i0 < num_words * 32; i0 += THREADS) {
     const int i = i0 + lane;
     const uint32_t k = i < n ? keys[i] : 0u;
@@ -713,7 +711,10 @@ kara_status launch_sparse_d(const SparseArgs& a, cudaStream_t stream) {
   launch_pdl(page_score_kernel<D>, dim3(static_cast<unsigned>(most < wave ? most : wave)),
              dim3(kScoreThreads), 0, stream, a);
   const dim3 rows(static_cast<unsigned>(a.B * a.Hkv));
-  launch_pdl(page_select_kernel<D>, rows, dim3(kSelThreads), 0, stream, a);
+  if (static_cast<int64_t>(a.B) * a.Hkv <= sms && a.max_blocks > 1024)
+    launch_pdl(page_select_kernel<D, 1024>, rows, dim3(1024), 0, stream, a);
+  else
+    launch_pdl(page_select_kernel<D, 512>, rows, dim3(512), 0, stream, a);
   return check_launch("paged_sparse_attn");
 }
 
