@@ -142,23 +142,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
   if (threadIdx.x == 0) a.head->tail_pages = line;
 }
 
-// 2^x of a pair on the FMA pipe, as ex2_fma2, but NaN for NaN: the power of two is a factor
-// instead of an addition to the bits.
-__device__ __forceinline__ float2 ex2_poly2(float2 x) {
-  x.x = fmax_nan(x.x, -125.0f);
-  x.y = fmax_nan(x.y, -125.0f);
-  const float2 shifter = make_float2(12582912.0f, 12582912.0f);
-  const float2 t = fadd2(x, shifter);
-  const float2 f = fsub2(x, fsub2(t, shifter));
-  float2 p = ffma2(make_float2(0.009570102207362652f, 0.009570102207362652f), f,
-                   make_float2(0.05591785907745361f, 0.05591785907745361f));
-  p = ffma2(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
-  p = ffma2(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
-  p = ffma2(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
-  return fmul2(p, make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
-                              __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000)));
-}
-
 // Items of up to kRows query rows go to team 0 alone, larger ones half to each team.
 __device__ __forceinline__ int team0_rows(int rows) { return rows > kRows ? (rows + 1) / 2 : rows; }
 
@@ -249,14 +232,14 @@ struct PfxSmem {
   static constexpr uint32_t q_off = 0;
   static constexpr uint32_t kv_off = 2 * kTile;
   static constexpr uint32_t bar_off = kv_off + kStages * kTile;
-  static constexpr int kBars = 2 * kStages + 2 + 3 + 4 + 2 + 2 + 8;
+  static constexpr int kBars = 2 * kStages + 2 + 3 + 4 + 2 + 2 + 8 + 1;
   static constexpr uint32_t bytes = bar_off + kBars * 8 + 16;
 };
 
 // The shared pages of all groups. Per key tile of 128 keys the products of 256 query rows take 2050
-// cycles of the tensor cores (d = 128) and their exponentials 1540 of the exponential unit, where a
-// quarter of them go to the FMA pipe; K and V of the tile take 2800 cycles of an SM's share of
-// HBM. So HBM bounds groups of up to about 128 query rows, products and exponentials larger ones,
+// cycles of the tensor cores (d = 128) and their exponentials 2050 of the exponential unit (moving a
+// quarter of them to the FMA pipe changed nothing); K and V of the tile take 2800 cycles of an
+// SM's share of HBM. So HBM bounds groups of up to about 128 query rows, products and exponentials larger ones,
 // whose softmax and products alternate between two teams of 128 rows. Rows live in tensor memory:
 // S and P of a row share columns, one thread owns the row, no statistics cross threads.
 // Measured: 128 rows of 28 heads behind 32K slots 76 us, 0.80 PFLOP/s (48 % of measured); 1 to 15
@@ -281,7 +264,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   uint64_t* o_full = p_full + 4;              // [2] O += P V done
   uint64_t* drained = o_full + 2;
   uint64_t* turn = drained + 2;               // [team][quad]: the warp may exponentiate
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
+  uint64_t* handover = turn + 8;              // one team's items after two teams', or before
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(handover + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = warp_id(), lane = lane_id();
 
@@ -301,6 +285,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     mbar_init(&drained[0], 1);
     mbar_init(&drained[1], 1);
     for (int i = 0; i < 8; ++i) mbar_init(&turn[i], 1);
+    mbar_init(handover, 8);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -490,6 +475,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     const float2 cs2 = make_float2(a.cs, a.cs);
     uint32_t s_ph[3] = {0, 0, 0}, o_ph = 0;   // o_ph: parity of the next product to complete
     uint32_t t_ph = w == 0 ? 1 : 0;           // team 0 goes first
+    uint32_t h_ph = 0;
+    int before = 0;                           // teams of the segment before (0: none)
     bool aborted = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!aborted) aborted = !wait_warp(bar, parity, abort_flag);
@@ -498,8 +485,19 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int rows0 = team0_rows(sg.rows);
       const int row0 = w == 0 ? 0 : rows0;      // the team's rows of the item
       const int live = w == 0 ? rows0 : sg.rows - rows0;
-      if (live <= 0) continue;
       const bool one_team = sg.rows <= kRows;
+      // A team on its own also uses the other's S buffer. So where segments of one team and of two
+      // follow each other, both teams finish what they have before either starts (its issuer
+      // waits for the team's queries).
+      const int teams = one_team ? 1 : 2;
+      if (before != 0 && before != teams) {
+        if (lane == 0) mbar_arrive(handover);
+        wait(handover, h_ph);
+        h_ph ^= 1;
+        if (aborted) break;
+      }
+      before = teams;
+      if (live <= 0) continue;
       const bool warp_on = quad * 32 < live;
       // the warp's 32 query rows into the swizzled tile, 16 bytes per lane, all in flight at once
       // (rows past the last: copies of it, whose results are not read)
@@ -621,7 +619,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 x = ffma2(make_float2(v[c + e], v[c + e + 1]), cs2, nb2);
-              const float2 p = e % 8 == 6 ? ex2_poly2(x) : make_float2(ex2(x.x), ex2(x.y));
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
               sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], p);
               const __nv_bfloat162 pb = __floats2bfloat162_rn(p.x, p.y);
               u[e / 2] = *reinterpret_cast<const uint32_t*>(&pb);

@@ -735,3 +735,17 @@ def test_binding_refuses_tensors_that_do_not_fit():
             call(**bad)
     given = torch.empty_like(qc)
     assert sparse(out=given) is given and prefix(out=given) is given
+
+
+def test_prefix_items_of_one_and_of_two_teams_in_turn():
+    """Groups of 2 and of 40 rows by turns, several per block: items for one tensor-core tile
+    follow items for two and the other way round. Run a few times: the result does not depend on
+    who is ahead."""
+    rows = [2, 40] * 24
+    pages = [11, 9, 17, 24] * 12
+    c, ptr = prefix_cache(77, rows, pages, 4, 128)
+    q = bf16(c.gen, len(c.lengths), 32, 128)
+    out = check_prefix(c, q, ptr, pages)
+    for _ in range(20):
+        again = K.paged_prefix_attn(q.cuda(), c.kd, c.vd, c.pool, i32(ptr), i32(pages))
+        assert torch.equal(out, again)
