@@ -390,9 +390,9 @@ __device__ __forceinline__ double exact_score(const SparseArgs& a, int b, int g,
     for (int j = 0; j < 4; ++j) {
       auto up = [](uint32_t w) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
       const float2 q = up(xw[j]), p = up(lw[j]), r = up(uw[j]);
-      // a product of two bf16 numbers is exact in fp32
-      sum[0] += static_cast<double>(q.x * (q.x < 0.f ? p.x : r.x));
-      sum[1] += static_cast<double>(q.y * (q.y < 0.f ? p.y : r.y));
+      // a product of two bf16 numbers is exact in fp64
+      sum[0] += static_cast<double>(q.x) * static_cast<double>(q.x < 0.f ? p.x : r.x);
+      sum[1] += static_cast<double>(q.y) * static_cast<double>(q.y < 0.f ? p.y : r.y);
     }
   }
   double best = sum[0] + sum[1];
@@ -557,7 +557,8 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SparseArgs a
   }
   const float t = tkey == 0u ? __int_as_float(0x7fc00000)
                              : __uint_as_float((tkey & 0x80000000u) ? tkey ^ 0x80000000u : ~tkey);
-  const float margin = 2.f * kScoreErr * s.err;
+  // the second part: fp32 products below 2^-126 may vanish, 2 d <= 256 of them
+  const float margin = 2.f * kScoreErr * s.err + 1e-35f;
   // every page: surely among the best (a key above that of t + margin), surely not (below that of
   // t - margin), or near the border; a NaN among them leaves everything near
   const bool nan = !(t + margin == t + margin) || !(t - margin == t - margin);

@@ -283,7 +283,8 @@ def test_sparse_matches_oracle(name, new_slots):
     assert torch.equal(out, again)                   # without sel, and deterministic
 
 
-@pytest.mark.parametrize("kind", ["zero_query", "equal_pages", "near_ties", "huge", "two_values"])
+@pytest.mark.parametrize("kind", ["zero_query", "equal_pages", "near_ties", "huge", "vast", "tiny",
+                                  "two_values"])
 def test_sparse_selection_at_the_border(kind):
     """Scores that fp32 cannot tell apart, or that are equal: the selection is still that of the
     exact scores, ties to the lower page."""
@@ -301,6 +302,12 @@ def test_sparse_selection_at_the_border(kind):
     elif kind == "huge":                             # fp32 sums overflow for some pages
         c.k[::3] *= 2.0 ** 100
         q *= 2.0 ** 24
+    elif kind == "vast":                             # so do products
+        c.k[::3] *= 2.0 ** 100
+        q *= 2.0 ** 100
+    elif kind == "tiny":                             # fp32 products vanish
+        c.k *= 2.0 ** -90
+        q *= 2.0 ** -60
     else:
         c.k[:] = torch.where(torch.rand(c.num_blocks, 1, 1, 1, generator=c.gen) < 0.5, 1.0, -1.0)
         q = q.abs()
