@@ -63,7 +63,12 @@ constexpr int kPlanThreads = 256;
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // few groups stay in shared memory: the rows' searches would wait for L2 at every step
+  constexpr int kNear = kPlanThreads;
   __shared__ RowItems<kPlanThreads> items;
+  __shared__ PrefixGroup near_groups[kNear];
+  __shared__ int near_ptr[kNear];
+  const bool near = a.num_groups <= kNear;
   long long flat = 0;
   for (int j0 = 0; j0 < a.num_groups; j0 += kPlanThreads) {
     const int j = j0 + static_cast<int>(threadIdx.x);
@@ -94,6 +99,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     if (j < a.num_groups) {
       gr.flat = flat + items.start[threadIdx.x];
       a.groups[j] = gr;
+      if (near) {
+        near_groups[j] = gr;
+        near_ptr[j] = a.group_ptr[j];
+      }
     }
     flat += items.start[kPlanThreads];
   }
@@ -112,11 +121,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
       int lo = 0, hi = a.num_groups;             // ptr[lo] <= i < ptr[hi] where there is one
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.group_ptr[mid] <= i) lo = mid;
+        if ((near ? near_ptr[mid] : a.group_ptr[mid]) <= i) lo = mid;
         else hi = mid;
       }
       a.row_group[i] = lo;
-      const PrefixGroup gr = a.groups[lo];
+      const PrefixGroup gr = near ? near_groups[lo] : a.groups[lo];
       if (i >= gr.first && i < gr.first + gr.rows) {
         const int row = a.group_rows != nullptr ? a.group_rows[i] : i;
         if (row < 0 || row >= a.B) {

@@ -756,3 +756,12 @@ def test_prefix_items_of_one_and_of_two_teams_in_turn():
     for _ in range(20):
         again = K.paged_prefix_attn(q.cuda(), c.kd, c.vd, c.pool, i32(ptr), i32(pages))
         assert torch.equal(out, again)
+
+
+def test_prefix_of_many_small_groups():
+    """More groups than the plan keeps in shared memory, rows of one slot and of none."""
+    rows = [1 + i % 3 for i in range(300)]
+    pages = [(i * 7) % 5 for i in range(300)]
+    c, ptr = prefix_cache(78, rows, pages, 1, 64)
+    q = bf16(c.gen, len(c.lengths), 5, 64)
+    check_prefix(c, q, ptr, pages)
