@@ -16,6 +16,7 @@
 #include <cuda.h>
 
 #include <cstdint>
+#include <limits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -777,7 +778,10 @@ kara_status launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
   a.extra = L.new_slots;
   a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
   a.negate = L.scale < 0.f ? 1 : 0;
+  // masked scores are -inf before they are scaled: a scale of 0 becomes the least number, which
+  // leaves them -inf and makes 5e-7 of the largest finite score
   a.cs = (a.negate ? -L.scale : L.scale) * 1.4426950408889634f;
+  if (a.cs == 0.f) a.cs = std::numeric_limits<float>::denorm_min();
   // the same maps as the streaming kernel's: one page of one KV head, 64 channels per box
   const uint64_t dims[4] = {static_cast<uint64_t>(L.D), static_cast<uint64_t>(L.Hkv), 16,
                             static_cast<uint64_t>(L.num_blocks)};

@@ -418,6 +418,13 @@ def test_prefix_peaked_rows(scale):
     check_prefix(c, bf16(c.gen, 8, 8, 128, scale=2.0), ptr, [40, 24], scale=scale)
 
 
+@pytest.mark.parametrize("pages", [1, 11, 20])
+def test_prefix_without_logits(pages):
+    """scale = 0: the plain mean of the values, with a prefix that ends inside a key tile."""
+    c, ptr = prefix_cache(56, [5], [pages], 2, 128)
+    check_prefix(c, bf16(c.gen, 5, 8, 128, scale=2.0), ptr, [pages], scale=0.0)
+
+
 def test_prefix_with_rows_in_any_order():
     """group_rows: members anywhere in the batch; rows in no group keep their output; a row
     listed twice is computed."""
