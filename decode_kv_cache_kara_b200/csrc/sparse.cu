@@ -197,7 +197,8 @@ __device__ __forceinline__ uint64_t order_key(double x) {
   return (b >> 63) ? ~b : b | 0x8000000000000000ull;
 }
 
-constexpr int kListMinPages = 2;                 // selected pages that are worth a warp
+constexpr int kListMinPages = 4;                 // selected pages that are worth a warp (128 of one
+                                                 // sequence: 24.6 us, with 2 25.3, with 1 28.3)
 constexpr int kSelBits = 10;
 constexpr int kSelKeys = 4096;                   // pages whose keys stay in shared memory
 constexpr int kDigit = 8;                        // bits of a score that one pass settles
@@ -411,15 +412,19 @@ __device__ __forceinline__ double exact_score(const SparseArgs& a, int b, int g,
 // ascending order from any order of work.
 // What bounds it is latency: about 15 dependent steps (a load, a barrier, a first fetch of code
 // each), 5 us for a row of 250 pages. 1024 threads where every block has an SM to itself and rows
-// can be long (one sequence of 4K pages 31.8 -> 30.0 us), else 512 (512 rows of 600 pages 154 us
-// against 164 with 1024 and 153 with 256; 32 sequences of 257 pages 38.6 against 38.9 and 38.2).
+// can be long (one sequence of 4K pages: its call 27.6 -> 25.3 us), else 512 (512 rows of 600 pages
+// 149 us against 158 with 1024 and 148 with 256; 32 sequences of 257 pages 34.5, 35.1 and 34.1).
 template <int D, int THREADS>
 __global__ void __launch_bounds__(THREADS) page_select_kernel(const SparseArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ SelectSmem<THREADS> s;
   const int bg = blockIdx.x, b = bg / a.Hkv, g = bg % a.Hkv;
   const int lane = lane_id();
+  // What needs no scores comes before the wait for them: the lengths were written, and the last
+  // call's lists read, before the score kernel was let start.
+  auto follow = [] {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  };
   const int np = seq_pages(a, b);
   int32_t* sel = a.sel + static_cast<size_t>(bg) * a.pages;
   if (threadIdx.x == 0 && g == 0) {
@@ -429,6 +434,7 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SparseArgs a
   }
   if (np <= a.pages) {                           // everything fits
     for (int i = threadIdx.x; i < a.pages; i += THREADS) sel[i] = i < np ? i : -1;
+    follow();
     return;
   }
   const int first = a.sink, last = np - a.recent;   // pages [first, last) compete
@@ -437,7 +443,10 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SparseArgs a
   const float2* score = a.score + static_cast<size_t>(bg) * a.max_blocks + first;
   for (int i = threadIdx.x; i < a.sink; i += THREADS) sel[i] = i;
   for (int i = threadIdx.x; i < a.recent; i += THREADS) sel[a.sink + want + i] = last + i;
-  if (want == 0) return;
+  if (want == 0) {
+    follow();
+    return;
+  }
   int32_t* near_page = a.near_page + static_cast<size_t>(bg) * a.max_blocks;
   double* near_score = a.near_score + static_cast<size_t>(bg) * a.max_blocks;
   const int num_words = (n + 31) / 32;
@@ -459,6 +468,7 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SparseArgs a
   constexpr int kSlots = kDigitBins + kDigitBins / 8;
 #pragma unroll 1
   for (int i = threadIdx.x; i < kSlots; i += THREADS) s.hist[i] = 0;
+  follow();
   float err = 0.f;
   uint32_t klo = 0xffffffffu, khi = 0u;
 #pragma unroll 4

@@ -104,9 +104,10 @@ __global__ void __launch_bounds__(kStrThreads, kStrBlocks)
 page_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const StreamArgs a) {
   static_assert(G <= 8, "at most 8 query heads per KV head");
-  // LIST follows the kernels that wrote its line and lists. Otherwise it runs beside the kernel
-  // before it, reads nothing that one writes, and waits for it at its end.
-  if constexpr (LIST) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The line was written before the kernel that this one follows: that one let it start only when
+  // its own wait was over. LIST waits for it before the first list is read; otherwise the two run
+  // side by side, and the wait comes at the end.
+  bool waited = false;
   constexpr int kStages = str_stages<D>();
   constexpr int NCH = D / 64;                 // 64-channel chunks per row
   constexpr int KS = D / 16;                  // k-steps of S^T, m-tiles of O^T
@@ -177,10 +178,14 @@ page_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
         qb[ks][1] = row_ok ? qrow[ks * 8 + 4 + tig] : 0u;
       }
     };
-    int pages_cu = load_pages(cu), pages_nu = load_pages(nu);
-    int ids_cu = load_ids(cu, pages_cu), ids_nu = load_ids(nu, pages_nu);
     uint32_t qb[KS][2];
     load_q(cu, qb);
+    if (LIST && !waited) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      waited = true;
+    }
+    int pages_cu = load_pages(cu), pages_nu = load_pages(nu);
+    int ids_cu = load_ids(cu, pages_cu), ids_nu = load_ids(nu, pages_nu);
 
     // Stream entries: a piece contributes 2 * np entries, K pages then V pages.
     int ustart = issued;     // stream index of cu's first entry
@@ -384,16 +389,16 @@ page_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
     for (int st = 0; st < kStages; ++st)
       if ((pending >> st) & 1u) mbar_wait(&my_bars[st], (phase >> st) & 1, &give_up, a.status);
   }
-  if constexpr (!LIST) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Join of a row's partials (m, l, o), base 2:
 //     m = max m_i,  l = sum 2^(m_i - m) l_i,  out = sum 2^(m_i - m) o_i / l.
-// SHARE warps per (list position, query head) take its partials in turn, each with a batch of them in
-// flight and a running (m, l, o) of its own, so that a partial is read once and without waiting
+// SHARE warps per (list position, query head) take its partials in turn, each with a batch of them
+// in flight and a running (m, l, o) of its own, so that a partial is read once and without waiting
 // for the maximum; a lane owns D / 32 channels. One warp each where the heads alone fill the SMs
-// (3584 heads 157 -> 153 us and 146 -> 143 us for their calls), else four (896 heads 40.5 -> 38.8,
-// 32 heads of 64 partials 34 -> 30).
+// (3584 heads 153 -> 149 us and 144 -> 139.5 us for their calls), else four (896 heads 35.9 -> 34.4,
+// 32 heads of 64 partials 30.2 -> 25.3).
 constexpr int kJoinWarps = 4;        // per block
 constexpr unsigned kJoinMany = 2048;
 
@@ -412,7 +417,6 @@ struct JoinArgs {
 
 template <int D, int SHARE>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int V = D / 32;
   constexpr int kBatch = SHARE == 1 ? 8 : 4;
   __shared__ float red_o[kJoinWarps][D];
@@ -420,11 +424,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs a)
   const int lane = lane_id(), warp = warp_id() % SHARE;
   const int head = static_cast<int>(blockIdx.x) * (kJoinWarps / SHARE) + warp_id() / SHARE;
   const int i = head / a.Hq, h = head - i * a.Hq;
-  if (i >= a.B) return;
+  if (i >= a.B) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int4 rw = a.line.rows[i];
   const int next = i + 1 < a.B ? a.line.rows[i + 1].w : -1;
   const int total = *a.line.total;
-  if (rw.x < 0) return;                          // not in a group: its output stays as it was
+  if (rw.x < 0) {                                // not in a group: its output stays as it was
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int len = (next < 0 ? total : next) - rw.w;
   int r0 = 0, ntail = 0;
   if (len > 0) {
@@ -455,6 +465,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs a)
     }
   }
   const int parts = npre + ntail;
+  // the line and the plan were written before the kernel that this one follows was let start
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float m = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
