@@ -14,7 +14,7 @@
 //           near the border, and those are scored again in fp64.
 //   attend  the streaming kernel over the chosen pages, and its join (stream.cu).
 // 128 sequences of 2K to 16K slots, 28 query and 4 KV heads, 128 pages each: score 30 us (147 MB,
-// 75 % of measured HBM), select 17 us, attend 97 us, join 8 us (from cold caches).
+// 75 % of measured HBM), select 17 us, attend 97 us, join 7 us (from cold caches).
 #include <cstdint>
 
 #include "common.cuh"
