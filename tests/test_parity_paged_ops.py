@@ -772,3 +772,44 @@ def test_prefix_of_many_small_groups():
     c, ptr = prefix_cache(78, rows, pages, 1, 64)
     q = bf16(c.gen, len(c.lengths), 5, 64)
     check_prefix(c, q, ptr, pages)
+
+
+def test_calls_in_a_row_share_a_workspace():
+    """Calls of other shapes and lengths follow each other in one stream and one workspace, with no
+    wait in between: a kernel starts before the one it follows has ended."""
+    big = Cache(79, [900, 40, 3000, 700], 4, 128, room=32)
+    small = Cache(80, [2500, 17], 2, 64, room=32)
+    shared, ptr = prefix_cache(81, [9, 4], [30, 11], 2, 128)
+    qb, qs, qp = (bf16(x.gen, len(x.lengths), h, x.d).cuda()
+                  for x, h in ((big, 28), (small, 4), (shared, 8)))
+    bb, bs = big.bounds().cuda(), small.bounds().cuda()
+    gp, pp = i32(ptr), i32([30, 11])
+    sel_b = torch.empty(4, 4, 20, dtype=torch.int32, device="cuda")
+    sel_s = torch.empty(2, 2, 7, dtype=torch.int32, device="cuda")
+
+    def sweep(**kw):
+        out = []
+        for step in range(6):
+            for new in (0, 1):
+                out.append(K.paged_sparse_attn(qb, big.kd, big.vd, bb, big.pool, 20, 1, 2,
+                                               new_slots=new, sel=sel_b, **kw))
+                out.append(sel_b.clone())
+                out.append(K.paged_sparse_attn(qs, small.kd, small.vd, bs, small.pool, 7,
+                                               new_slots=new, sel=sel_s, **kw))
+                out.append(K.paged_prefix_attn(qp, shared.kd, shared.vd, shared.pool, gp, pp,
+                                               new_slots=new, **kw))
+                out.append(K.paged_sparse_attn(qb, big.kd, big.vd, bb, big.pool, 300, **kw))
+                if "workspace" not in kw:
+                    torch.cuda.synchronize()
+            big.pool.ctx_len.add_(3)
+            small.pool.ctx_len.add_(5)
+        big.pool.ctx_len.sub_(18)
+        small.pool.ctx_len.sub_(30)
+        torch.cuda.synchronize()
+        return out
+
+    want = sweep()
+    room = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    for _ in range(10):
+        for a, b in zip(sweep(workspace=room), want):
+            assert torch.equal(a, b)
