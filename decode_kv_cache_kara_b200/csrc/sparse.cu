@@ -178,8 +178,10 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) page_score_kernel
         e1 = fmaxf(e1, __shfl_xor_sync(0xffffffffu, e1, off));
       }
       float2* dst = a.score + (static_cast<size_t>(b) * a.Hkv + g) * a.max_blocks + p0;
-      if (tig == 0 && p0 + grp < np) dst[grp] = make_float2(m0, e0);
-      if (tig == 1 && p0 + grp + 8 < np) dst[grp + 8] = make_float2(m1, e1);
+      // a page that the table does not hold goes last, as exact_score has it
+      if (tig == 0 && p0 + grp < np) dst[grp] = make_float2(blk_lo >= 0 ? m0 : -INFINITY, e0);
+      if (tig == 1 && p0 + grp + 8 < np)
+        dst[grp + 8] = make_float2(blk_hi >= 0 ? m1 : -INFINITY, e1);
     }
     base += total;
   }

@@ -1,0 +1,57 @@
+"""GPU parity of the operators around the paged cache at the edges of their contracts: pages that
+the table does not hold, scores and values that are not finite, malformed inputs one at a time.
+
+Tolerances are those of test_parity_paged_ops.py; page numbers, bounds, cache bytes and status
+codes are exact.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from decode_kv_cache_kara_b200 import kara as K
+from oracle import paged_ops as op
+from tests import helpers as H
+from tests.test_parity_paged_ops import (PAGE, Cache, append_inputs, attention_close, bf16, i32,
+                                         inv_freq, prefix_cache, rotation_close)
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------- sparse attention
+
+def select_without(c, q, bounds, pages, bad):
+    """The selection of sequence 0 when the pages `bad` have no score."""
+    n = -(-int(c.lengths[0]) // PAGE)
+    blocks = np.where(np.isin(np.arange(n), bad), 0, c.table[0, :n])
+    s = op.page_scores(H.f64(q[0]), H.f64(bounds), blocks)
+    s[:, bad] = -np.inf
+    return np.stack([op.select_pages(s[g], pages, 1, 2) for g in range(c.hkv)])
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("bad", [[10], [3, 4, 20, 21, 22], list(range(1, 40))])
+def test_a_competing_page_without_a_block_goes_last(bad, hq):
+    """All scores are below 0; a page whose block id is out of range is chosen only where nothing
+    else is left, and adds nothing to the output."""
+    pages = 12
+    c = Cache(91, [16 * 44 - 3], 2, 64)
+    c.k = -c.k.abs()
+    c.kd = c.k.cuda()
+    q = bf16(c.gen, 1, hq, 64).abs()
+    bounds = c.bounds()
+    for i, p in enumerate(bad):
+        c.table[0, p] = (c.num_blocks + 5, -1, 2 ** 31 - 1)[i % 3]
+    sel = torch.empty((1, 2, pages), dtype=torch.int32, device="cuda")
+    status = K.new_status()
+    out = K.paged_sparse_attn(q.cuda(), c.kd, c.vd, bounds.cuda(), c.make_pool(), pages, sel=sel,
+                              status=status)
+    assert K.read_status(status) == K.ERR_BAD_BLOCK
+    want = select_without(c, q, bounds, pages, bad)
+    assert np.array_equal(H.i32(sel)[0], want)
+    read = np.where(np.isin(want, bad), -1, want)[None]
+    ref, mag = op.sparse_attention(H.f64(q), H.f64(c.k), H.f64(c.v), read, c.table, c.lengths,
+                                   0.125, PAGE)
+    attention_close(out, ref, mag)
