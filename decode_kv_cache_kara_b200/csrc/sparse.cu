@@ -572,8 +572,10 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SparseArgs a
   // the second part: fp32 products below 2^-126 may vanish, 2 d <= 256 of them
   const float margin = 2.f * kScoreErr * s.err + 1e-35f;
   // every page: surely among the best (a key above that of t + margin), surely not (below that of
-  // t - margin), or near the border; a NaN among them leaves everything near
-  const bool nan = !(t + margin == t + margin) || !(t - margin == t - margin);
+  // t - margin), or near the border. An infinite margin says that fp32 sums overflowed, so that even
+  // a score that is NaN in fp32 (the lowest key) may belong to the best: everything is near then, as
+  // when t is NaN or infinite.
+  const bool nan = !(margin < INFINITY) || !(t + margin == t + margin) || !(t - margin == t - margin);
   const uint32_t key_up = nan ? 0xffffffffu : order_key(t + margin);
   const uint32_t key_low = nan ? 0u : order_key(t - margin);
 #pragma unroll 2

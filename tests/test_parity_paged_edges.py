@@ -55,3 +55,22 @@ def test_a_competing_page_without_a_block_goes_last(bad, hq):
     ref, mag = op.sparse_attention(H.f64(q), H.f64(c.k), H.f64(c.v), read, c.table, c.lengths,
                                    0.125, PAGE)
     attention_close(out, ref, mag)
+
+
+@pytest.mark.parametrize("hq", [2, 14, 16])
+def test_selection_where_fp32_scores_are_not_numbers(hq):
+    """Pages of one repeated key whose products with queries of mixed sign overflow: in fp32 their
+    scores are inf - inf, in 64 bits they are numbers and belong to the largest."""
+    hkv, d, pages = 2, 128, 20
+    c = Cache(92, [700, 300], hkv, d)
+    c.k[:] = c.k[:, :1]
+    c.k[::3] *= 2.0 ** 100
+    c.kd = c.k.cuda()
+    q = bf16(c.gen, 2, hq, d) * 2.0 ** 40
+    bounds = c.bounds()
+    sel = torch.empty((2, hkv, pages - 5), dtype=torch.int32, device="cuda")
+    K.paged_sparse_attn(q.cuda(), c.kd, c.vd, bounds.cuda(), c.pool, pages - 5, sel=sel)
+    for b, n in enumerate(c.lengths):
+        s = op.page_scores(H.f64(q[b]), H.f64(bounds), c.table[b, :-(-int(n) // PAGE)])
+        for g in range(hkv):
+            assert np.array_equal(H.i32(sel[b, g]), op.select_pages(s[g], pages - 5, 1, 2))
