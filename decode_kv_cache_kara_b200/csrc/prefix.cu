@@ -330,10 +330,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     const bool elected = elect_one();
     while (ok && cur.next(a, sg)) {
       const int32_t* table = a.block_table + static_cast<size_t>(sg.row0) * a.max_blocks;
-      // pages past the prefix in its last tile: its last page again (their weights are 0)
+      // pages past the prefix in its last tile: the block behind the pool, which a copy fills with
+      // zeros (their weights are 0, and so are the values: 0 x inf would be NaN)
       auto block_of = [&](int kt) -> int {
         if (lane >= kTilePages) return 0;
-        int blk = table[min(kt * kTilePages + lane, sg.pages - 1)];
+        const int page = kt * kTilePages + lane;
+        if (page >= sg.pages) return a.num_blocks;
+        int blk = table[page];
         if (blk < 0 || blk >= a.num_blocks) {
           report(a.status, KARA_ERR_BAD_BLOCK);
           blk = 0;

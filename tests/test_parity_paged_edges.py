@@ -74,3 +74,26 @@ def test_selection_where_fp32_scores_are_not_numbers(hq):
         s = op.page_scores(H.f64(q[b]), H.f64(bounds), c.table[b, :-(-int(n) // PAGE)])
         for g in range(hkv):
             assert np.array_equal(H.i32(sel[b, g]), op.select_pages(s[g], pages - 5, 1, 2))
+
+
+# -------------------------------------------------------------------- values that are not finite
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("pages", [1, 3, 11, 15])
+def test_infinity_in_the_last_shared_page(pages, d):
+    """A prefix that ends inside a key tile, with infinite values in its last page: infinite
+    outputs in those channels, not NaN, and the other channels keep their values."""
+    c, ptr = prefix_cache(93, [5], [pages], 2, d)
+    q = bf16(c.gen, 5, 8, d)
+    last = int(c.table[0, pages - 1])
+    c.vd[last, 3, 0, 7] = float("inf")
+    c.vd[last, 15, 1, 20] = float("-inf")
+    status = K.new_status()
+    out = K.paged_prefix_attn(q.cuda(), c.kd, c.vd, c.pool, i32(ptr), i32([pages]), status=status)
+    assert K.read_status(status) == 0
+    assert (out[:, :4, 7] == float("inf")).all() and (out[:, 4:, 20] == float("-inf")).all()
+    ref, mag = op.dense_attention(H.f64(q), H.f64(c.k), H.f64(c.v), c.table, c.lengths,
+                                  1 / math.sqrt(d), PAGE)
+    fine = np.ones(ref.shape, bool)
+    fine[:, :4, 7] = fine[:, 4:, 20] = False
+    attention_close(out.cpu()[torch.from_numpy(fine)], ref[fine], mag[fine])
