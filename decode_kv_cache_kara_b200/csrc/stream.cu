@@ -394,6 +394,8 @@ page_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
 
 // Join of a row's partials (m, l, o), base 2:
 //     m = max m_i,  l = sum 2^(m_i - m) l_i,  out = sum 2^(m_i - m) o_i / l.
+// A partial is empty where its l is 0, not where its m is -inf: scores that are all NaN leave no
+// maximum, and their l and o are NaN.
 // SHARE warps per (list position, query head) take its partials in turn, each with a batch of them
 // in flight and a running (m, l, o) of its own, so that a partial is read once and without waiting
 // for the maximum; a lane owns D / 32 channels. One warp each where the heads alone fill the SMs
@@ -491,16 +493,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs a)
     float top = m;
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) top = fmaxf(top, ml[e].x);
-    if (top == -INFINITY) continue;
-    const float f = ex2(m - top);
+    const float base = top == -INFINITY ? 0.f : top;
+    const float f = ex2(m - base);
     m = top;
     l *= f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= f;
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) {
-      if (ml[e].x == -INFINITY) continue;        // nothing in it (or none: o was not read)
-      const float w = ex2(ml[e].x - m);
+      if (ml[e].y == 0.f) continue;              // nothing in it (or none: o was not read)
+      const float w = ex2(ml[e].x - base);
       l += w * ml[e].y;
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[e][v], acc[v]);
@@ -527,10 +529,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs a)
   float top = red_m[0];
 #pragma unroll
   for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, red_m[w]);
+  if (top == -INFINITY) top = 0.f;
   float sum = 0.f, r0o = 0.f, r1o = 0.f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) {
-    if (red_m[w] == -INFINITY) continue;
+    if (red_l[w] == 0.f) continue;
     const float f = ex2(red_m[w] - top);
     sum += f * red_l[w];
     r0o = fmaf(f, red_o[w][c], r0o);

@@ -97,3 +97,37 @@ def test_infinity_in_the_last_shared_page(pages, d):
     fine = np.ones(ref.shape, bool)
     fine[:, :4, 7] = fine[:, 4:, 20] = False
     attention_close(out.cpu()[torch.from_numpy(fine)], ref[fine], mag[fine])
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_nan_queries_and_lone_nan_keys_reach_the_output(rows):
+    """A NaN query's outputs are NaN, and so are those of a row whose only own key is NaN; the
+    others keep their values. `rows` takes both forms of the join."""
+    hq = 64
+    c, ptr = prefix_cache(94, [rows], [6], 8, 64, least=2)
+    c.lengths[0] = 6 * PAGE + 1                      # row 0: one key of its own
+    c.pool = c.make_pool()
+    q = bf16(c.gen, rows, hq, 64).cuda()
+    good = K.paged_prefix_attn(q, c.kd, c.vd, c.pool, i32(ptr), i32([6]))
+    bounds = c.bounds().cuda()
+    good_sparse = K.paged_sparse_attn(q, c.kd, c.vd, bounds, c.pool, 4)
+    c.kd[int(c.table[0, 6]), 0, 5] = float("nan")    # KV head 5
+    q[1, 9] = float("nan")
+    bad = torch.zeros((rows, hq), dtype=torch.bool, device="cuda")
+    bad[0, 40:48] = True
+    bad[1, 9] = True
+    out = K.paged_prefix_attn(q, c.kd, c.vd, c.pool, i32(ptr), i32([6]))
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], good[~bad])
+    out = K.paged_sparse_attn(q, c.kd, c.vd, bounds, c.pool, 4)
+    assert torch.isnan(out[bad]).all()
+    bad[1, 8:16] = True                              # NaN takes part in the group's selection
+    assert torch.equal(out[~bad], good_sparse[~bad])
+
+
+def test_a_context_of_one_nan_key():
+    c = Cache(95, [1, 0, 5], 2, 128)
+    c.kd[int(c.table[0, 0]), 0] = float("nan")
+    q = bf16(c.gen, 3, 4, 128).cuda()
+    for out in (K.paged_sparse_attn(q, c.kd, c.vd, c.bounds().cuda(), c.pool, 4),
+                K.paged_prefix_attn(q, c.kd, c.vd, c.pool, i32([0, 1, 2, 3]), i32([0, 0, 0]))):
+        assert torch.isnan(out[0]).all() and (out[1] == 0).all() and torch.isfinite(out[2]).all()
