@@ -171,6 +171,11 @@ kara_status decode_impl(const void* q, const void* k_new, const void* v_new, con
   return launch_decode(L, stream);
 }
 
+// Whether the sizes of a pool can size a workspace (its pointers may be null here).
+bool sizes_ok(const kara_pool* pool) {
+  return pool != nullptr && pool->batch > 0 && pool->num_kv_heads > 0 && pool->head_dim > 0;
+}
+
 bool new_slots_ok(const kara_pool* pool, int32_t new_slots) {
   return new_slots >= 0 &&
          new_slots <= static_cast<int64_t>(pool->max_blocks_per_seq) * pool->page_size;
@@ -217,11 +222,12 @@ size_t kara_workspace_bytes(kara_op op, const kara_pool* pool, int32_t num_seqs,
       if (num_seqs <= 0 || k_or_budget <= 0) return 0;
       return lacache_workspace_bytes(num_seqs, k_or_budget);
     case KARA_OP_SPARSE:
-      if (pool == nullptr || pool->batch <= 0 || num_q_heads <= 0 || k_or_budget <= 0) return 0;
+      if (!sizes_ok(pool) || pool->max_blocks_per_seq <= 0 || num_q_heads <= 0 || k_or_budget <= 0)
+        return 0;
       return sparse_workspace_bytes(pool->batch, num_q_heads, pool->num_kv_heads, pool->head_dim,
                                     pool->max_blocks_per_seq, k_or_budget);
     case KARA_OP_PREFIX:
-      if (pool == nullptr || pool->batch <= 0 || num_q_heads <= 0) return 0;
+      if (!sizes_ok(pool) || num_q_heads <= 0) return 0;
       return prefix_workspace_bytes(pool->batch, num_q_heads, pool->num_kv_heads,
                                     pool->head_dim);
     default:

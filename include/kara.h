@@ -568,7 +568,8 @@ kara_status lacache_compact(const kara_layer_kv* layers, int32_t num_layers,
                             size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream);
 
 /*
- * kara_workspace_bytes - workspace size for one call (0 if the op needs none).
+ * kara_workspace_bytes - workspace size for one call (0 if the op needs none, or if a size that it
+ * goes by is not positive).
  *  KARA_OP_SCORE:   num_seqs, window, num_q_heads used.
  *  KARA_OP_COMPACT: num_seqs, window (the budget k goes in `k_or_budget`).
  *  KARA_OP_DECODE:  pool->batch, num_q_heads, head_dim, max_blocks_per_seq used.
