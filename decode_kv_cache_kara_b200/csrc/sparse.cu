@@ -15,6 +15,7 @@
 //   attend  the streaming kernel over the chosen pages, and its join (stream.cu).
 // 128 sequences of 2K to 16K slots, 28 query and 4 KV heads, 128 pages each: score 30 us (147 MB,
 // 75 % of measured HBM), select 17 us, attend 97 us, join 7 us (from cold caches).
+#include <algorithm>
 #include <cstdint>
 
 #include "common.cuh"
@@ -736,11 +737,15 @@ kara_status launch_sparse_d(const SparseArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t sparse_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks, int pages) {
-  return sparse_layout(B, Hq, Hkv, D, max_blocks, pages).total;
+  return sparse_layout(B, Hq, Hkv, D, max_blocks, std::min(pages, max_blocks)).total;
 }
 
 kara_status launch_sparse(const SparseLaunch& L, cudaStream_t stream) {
-  const SparseLayout lay = sparse_layout(L.B, L.Hq, L.Hkv, L.D, L.max_blocks, L.pages);
+  const SparseLayout lay = sparse_layout(L.B, L.Hq, L.Hkv, L.D, L.max_blocks,
+                                         std::min(L.pages, L.max_blocks));
+  // the caller's lists have num_pages entries each, the workspace's no more than the table (where
+  // every page is read, as every page then fits)
+  const int pages = L.sel != nullptr ? L.pages : std::min(L.pages, L.max_blocks);
   uint8_t* ws = static_cast<uint8_t*>(L.workspace);
   SparseArgs a;
   a.q = static_cast<const __nv_bfloat16*>(L.q);
@@ -760,7 +765,7 @@ kara_status launch_sparse(const SparseLaunch& L, cudaStream_t stream) {
   a.Hkv = L.Hkv;
   a.max_blocks = L.max_blocks;
   a.num_blocks = L.num_blocks;
-  a.pages = L.pages;
+  a.pages = pages;
   a.sink = L.sink;
   a.recent = L.recent;
   a.extra = L.new_slots;
@@ -773,7 +778,7 @@ kara_status launch_sparse(const SparseLaunch& L, cudaStream_t stream) {
   t.block_table = L.block_table;
   t.status = L.status;
   t.sel = a.sel;
-  t.sel_pages = L.pages;
+  t.sel_pages = pages;
   t.line.rows = a.rows;
   t.line.total = a.total;
   t.line.max_ranges = 0;

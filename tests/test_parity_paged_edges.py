@@ -131,3 +131,20 @@ def test_a_context_of_one_nan_key():
     for out in (K.paged_sparse_attn(q, c.kd, c.vd, c.bounds().cuda(), c.pool, 4),
                 K.paged_prefix_attn(q, c.kd, c.vd, c.pool, i32([0, 1, 2, 3]), i32([0, 0, 0]))):
         assert torch.isnan(out[0]).all() and (out[1] == 0).all() and torch.isfinite(out[2]).all()
+
+
+@pytest.mark.parametrize("pages", [9, 10, 2 ** 31 - 1])
+def test_more_pages_than_the_table_has(pages):
+    """num_pages at and beyond the table's width (9): attention over every slot, with the fixed
+    pages outnumbering the table too."""
+    c = Cache(96, [120, 3, 0, 77], 2, 64)
+    assert c.table.shape[1] == 9
+    q = bf16(c.gen, 4, 6, 64)
+    status = K.new_status()
+    for sink, recent in ((1, 2), (min(pages - 1, 2 ** 30), 1)):
+        out = K.paged_sparse_attn(q.cuda(), c.kd, c.vd, c.bounds().cuda(), c.pool, pages, sink,
+                                  recent, status=status)
+        assert K.read_status(status) == 0
+        ref, mag = op.dense_attention(H.f64(q), H.f64(c.k), H.f64(c.v), c.table, c.lengths, 0.125,
+                                      PAGE)
+        attention_close(out, ref, mag)
