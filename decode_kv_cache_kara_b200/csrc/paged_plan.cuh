@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "kara.h"
+
 namespace kara {
 
 // The pages that the streaming kernel reads form one line per KV head, row after row. Row i of
@@ -22,19 +24,25 @@ __device__ __forceinline__ int stream_ranges(const StreamLine& s, int total) {
   const int most = total / s.min_pages;
   return total == 0 ? 0 : most < 1 ? 1 : most < s.max_ranges ? most : s.max_ranges;
 }
-// n / d for n >= 0, d > 0: the 64-bit division only where n needs it.
-__device__ __forceinline__ long long divide(long long n, int d) {
-  return (n >> 32) == 0
+// n / d for n >= 0, d > 0: the 64-bit division only where one of them needs it.
+__host__ __device__ __forceinline__ long long divide(long long n, long long d) {
+  return ((n | d) >> 32) == 0
              ? static_cast<long long>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d))
              : n / d;
 }
+// A line of `total` units cut into `parts` equal parts: the first unit of part r, and the part that
+// holds unit u.
+__host__ __device__ __forceinline__ long long part_start(long long r, int parts, long long total) {
+  return divide(r * total, parts);
+}
+__host__ __device__ __forceinline__ int part_of(long long u, int parts, long long total) {
+  return static_cast<int>(divide((u + 1) * parts - 1, total));
+}
 // First page of range r of R on a line of `total` pages, and the range that holds page p.
 __device__ __forceinline__ int range_start(int r, int R, int total) {
-  return static_cast<int>(divide(static_cast<long long>(r) * total, R));
+  return static_cast<int>(part_start(r, R, total));
 }
-__device__ __forceinline__ int range_of(int p, int R, int total) {
-  return static_cast<int>(divide((static_cast<long long>(p) + 1) * R - 1, total));
-}
+__device__ __forceinline__ int range_of(int p, int R, int total) { return part_of(p, R, total); }
 
 // Shared prefixes: the work of all items (group, query tile, KV head) is one line of key tiles,
 // cut into equal parts, one per block.

@@ -189,8 +189,8 @@ struct SegCursor {
     pos = end = 0;
     j = 0;
     if (cta >= n) return;
-    pos = divide(total * cta, n);
-    end = divide(total * (cta + 1), n);
+    pos = part_start(cta, n, total);
+    end = part_start(cta + 1, n, total);
     int lo = 0, hi = a.num_groups;               // the last group with flat <= pos
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;

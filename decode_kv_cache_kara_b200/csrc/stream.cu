@@ -457,10 +457,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs a)
       // the item's first key is unit a0 of the line
       const long long a0 = gr.flat + kItemCost +
                            static_cast<long long>(t * a.Hkv + g) * (gr.ktiles + kItemCost);
-      const int work = static_cast<int>(a.head->total);
+      const long long work = a.head->total;
       const int ctas = a.head->ctas;
-      const int c0 = static_cast<int>(divide((a0 + 1) * ctas - 1, work));
-      npre = static_cast<int>(divide((a0 + gr.ktiles) * ctas - 1, work)) - c0 + 1;
+      const int c0 = part_of(a0, ctas, work);
+      npre = part_of(a0 + gr.ktiles - 1, ctas, work) - c0 + 1;
       row = static_cast<long long>(a.Hq) * gr.first +
             static_cast<long long>(t) * gr.item_rows * a.Hkv + static_cast<long long>(g) * rows_t +
             r + static_cast<long long>(kItemRows) * c0;

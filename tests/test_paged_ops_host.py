@@ -34,3 +34,39 @@ def test_sparse_workspace_ends_with_the_table(lib_path):
         return K.lib().kara_workspace_bytes(K.OP_SPARSE, ctypes.byref(p), 0, 0, 28, pages)
 
     assert size(1023) < size(1024) == size(1025) == size(2 ** 31 - 1)
+
+
+LINE = r"""
+#include <cstdio>
+#include "paged_plan.cuh"
+int main() {
+  const long long totals[] = {1, 5, 147, 148, 70000, 2147483647LL, 2147483648LL, 2163212288LL,
+                              4294967296LL, 5000000011LL, 30000000000LL};
+  for (long long total : totals)
+    for (int parts : {1, 2, 44, 148, 160}) {
+      if (parts > total) continue;
+      for (int r = 0; r < parts; ++r) {
+        const long long first = kara::part_start(r, parts, total);
+        const long long end = kara::part_start(r + 1, parts, total);
+        if (first >= end || kara::part_of(first, parts, total) != r ||
+            kara::part_of(end - 1, parts, total) != r) {
+          std::printf("%lld units, %d parts, part %d: [%lld, %lld)\n", total, parts, r, first, end);
+          return 1;
+        }
+      }
+    }
+  return 0;
+}
+"""
+
+
+def test_parts_of_a_work_line_past_32_bits(tmp_path):
+    """Where a part starts and which part holds a unit agree, for lines of more units than 32 bits
+    hold (many groups behind a long prefix; too much work to run)."""
+    src, exe = tmp_path / "line.cu", tmp_path / "line"
+    src.write_text(LINE)
+    run = subprocess.run([B.nvcc(), "-std=c++17", "-I", B.CSRC, "-I", B.INCLUDE, str(src), "-o",
+                          str(exe)] + B.ARCH, capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout
