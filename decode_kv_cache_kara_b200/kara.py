@@ -12,6 +12,7 @@ There is no CPU fallback: a missing library raises ``KaraLibraryError``.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import re
@@ -636,11 +637,17 @@ def _native():
     global _NATIVE
     if _NATIVE is None:
         lib()
-        if not os.path.exists(_build.NATIVE):
-            raise KaraLibraryError(f"{_build.NATIVE} is missing: build it with "
-                                   "`python -m decode_kv_cache_kara_b200.build`")
-        from . import _native as module
-        module.bind(library_path())
+        path = _build.native_path()
+        if not os.path.exists(path):
+            raise KaraLibraryError(f"{path} is missing (the module goes with one Python and torch): "
+                                   "build it with `python -m decode_kv_cache_kara_b200.build`")
+        try:
+            spec = importlib.util.spec_from_file_location(__package__ + "._native", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind(library_path())
+        except ImportError as e:
+            raise KaraLibraryError(f"cannot load {path}: {e}") from e
         _NATIVE = module
     return _NATIVE
 

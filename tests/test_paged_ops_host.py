@@ -1,8 +1,13 @@
 """Host side of the operators around the paged cache (CPU)."""
 
 import ctypes
+import os
 import subprocess
 import sys
+import sysconfig
+
+import pytest
+import torch
 
 from decode_kv_cache_kara_b200 import build as B
 from decode_kv_cache_kara_b200 import kara as K
@@ -70,3 +75,46 @@ def test_parts_of_a_work_line_past_32_bits(tmp_path):
     assert run.returncode == 0, run.stderr
     run = subprocess.run([str(exe)], capture_output=True, text=True)
     assert run.returncode == 0, run.stdout
+
+
+@pytest.fixture
+def small_build(monkeypatch, tmp_path):
+    """A build of one small source in a folder of its own, with a binding that does not compile."""
+    src = tmp_path / "one.cu"
+    src.write_text('extern "C" int kara_one() { return 1; }\n')
+    monkeypatch.setattr(B, "sources", lambda: [str(src)])
+    monkeypatch.setattr(B, "BUILD_DIR", str(tmp_path / "objects"))
+    monkeypatch.setattr(B, "LIB", str(tmp_path / "libone.so"))
+    monkeypatch.setattr(B, "_native_command", lambda out: [sys.executable, "-c", "raise SystemExit(3)"])
+    monkeypatch.setattr(B, "PKG", str(tmp_path))
+    return tmp_path
+
+
+def test_library_is_linked_where_the_binding_does_not_compile(small_build):
+    with pytest.raises(RuntimeError, match="binding"):
+        B.build()
+    assert ctypes.CDLL(B.LIB).kara_one() == 1
+
+
+def test_ensure_built_warns_without_the_binding(small_build):
+    with pytest.warns(UserWarning, match="binding failed"):
+        assert B.ensure_built() == B.LIB
+    assert ctypes.CDLL(B.LIB).kara_one() == 1
+
+
+def test_binding_is_named_for_its_python_and_torch(monkeypatch):
+    name = os.path.basename(B.native_path())
+    assert torch.__version__ in name and name.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    assert B.native_path() != name and B._native_stale()
+
+
+def test_missing_or_broken_binding_is_a_library_error(lib_path, monkeypatch, tmp_path):
+    monkeypatch.setattr(K, "_NATIVE", None)
+    path = tmp_path / "_native.so"
+    monkeypatch.setattr(B, "native_path", lambda: str(path))
+    with pytest.raises(K.KaraLibraryError, match="missing"):
+        K._native()
+    path.write_bytes(b"not a module")
+    with pytest.raises(K.KaraLibraryError, match="cannot load"):
+        K._native()
