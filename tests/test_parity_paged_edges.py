@@ -15,7 +15,8 @@ from decode_kv_cache_kara_b200 import kara as K
 from oracle import paged_ops as op
 from tests import helpers as H
 from tests.test_parity_paged_ops import (PAGE, Cache, append_inputs, attention_close, bf16, i32,
-                                         inv_freq, prefix_cache, rotation_close)
+                                         inv_freq, prefix_cache, rotation_close,
+                                         sparse_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +149,107 @@ def test_more_pages_than_the_table_has(pages):
         ref, mag = op.dense_attention(H.f64(q), H.f64(c.k), H.f64(c.v), c.table, c.lengths, 0.125,
                                       PAGE)
         attention_close(out, ref, mag)
+
+
+# ------------------------------------------------------------------- malformed inputs, one by one
+
+@pytest.mark.parametrize("cu", [[0, 4, 2, 9], [0, 4, 12, 9], [-1, 4, 6, 9], [0, 4, 6, 10],
+                                [3, 3, 9, 1], [2 ** 31 - 1, 2, 2, 9]])
+def test_append_skips_the_sequences_of_bad_token_counts(cu):
+    """A healthy cache: sequences whose range of tokens descends or leaves [0, tokens] are skipped
+    and reported, the others are appended; rows of no sequence stay as they were."""
+    tokens, hq, hkv, d = 9, 6, 2, 64
+    ctx = np.array([5, 20, 33])
+    c = Cache(97, [n + 16 for n in ctx], hkv, d)
+    c.lengths = ctx
+    pool = c.make_pool()
+    (q, k, v), dev = append_inputs(c, hq, tokens, True)
+    pos = np.arange(tokens) * 7
+    q_out = torch.full((tokens, hq, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    k_out = torch.full((tokens, hkv, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    status = K.new_status()
+    K.paged_rope_append(*dev, c.kd, c.vd, pool, inv_freq(d).cuda(), i32(pos), cu_tokens=i32(cu),
+                        q_out=q_out, k_out=k_out, status=status)
+    assert K.read_status(status) == K.ERR_INVALID_ARG
+    good = [b for b in range(3) if 0 <= cu[b] <= cu[b + 1] <= tokens]
+    assert 0 < len(good) < 3
+    at = np.concatenate([np.zeros((0, 3))] +
+                        [[(t, b, ctx[b] + i) for i, t in enumerate(range(cu[b], cu[b + 1]))]
+                         for b in good if cu[b] < cu[b + 1]]).astype(np.int64)
+    rows = np.unique(at[:, 0])
+    rest = np.setdiff1d(np.arange(tokens), rows)
+    rotation_close(q_out[rows], q[rows], pos[rows], inv_freq(d), False)
+    rotation_close(k_out[rows], k[rows], pos[rows], inv_freq(d), False)
+    assert (q_out[rest] == 5).all() and (k_out[rest] == 5).all()
+    kref, vref = H.bits(c.k), H.bits(c.v)
+    blk, row = c.table[at[:, 1], at[:, 2] // PAGE], at[:, 2] % PAGE
+    kref[blk, row] = H.bits(k_out)[at[:, 0]]
+    vref[blk, row] = H.bits(v)[at[:, 0]]
+    assert np.array_equal(H.bits(c.kd), kref) and np.array_equal(H.bits(c.vd), vref)
+
+
+@pytest.mark.parametrize("fault", ["past_table", "negative", "bad_block"])
+def test_bounds_and_sparse_report_one_fault(fault):
+    """One fault in one sequence of a healthy cache: its own code, and the other sequences' results
+    are right."""
+    c = Cache(98, [300, 75, 16, 0], 2, 64)
+    c.table = np.where(c.table < 0, c.table[1, 0], c.table)    # every entry names a block
+    q = bf16(c.gen, 4, 6, 64).cuda()
+    bounds = c.bounds()
+    _, ref, mag = sparse_reference(c, H.f64(q), H.f64(bounds), c.lengths, 6, 1, 2)
+    whole = K.paged_page_bounds(c.kd, c.make_pool())
+    if fault == "bad_block":
+        c.table[0, 11] = c.num_blocks
+    else:
+        c.lengths[0] = -1 if fault == "negative" else PAGE * c.table.shape[1] + 1
+    code = K.ERR_BAD_BLOCK if fault == "bad_block" else K.ERR_INVALID_ARG
+    pool = c.make_pool()
+    status = K.new_status()
+    out = K.paged_sparse_attn(q, c.kd, c.vd, bounds.cuda(), pool, 6, status=status)
+    assert K.read_status(status) == code
+    assert torch.isfinite(out).all()
+    attention_close(out[1:], ref[1:], mag[1:])
+    status = K.new_status()
+    got = K.paged_page_bounds(c.kd, pool, status=status)
+    assert K.read_status(status) == code
+    # the pages of the other sequences, and those of the first that are still named by its table
+    old = c.pool.block_table[0].cpu().numpy()
+    lost = old[11:12] if fault == "bad_block" else old[:300 // PAGE]
+    kept = np.setdiff1d(np.arange(c.num_blocks), lost)
+    assert torch.equal(got[kept], whole[kept]) and (got[lost] == 0).all()
+
+
+@pytest.mark.parametrize("fault", ["descends", "past_batch", "below_zero", "pages_negative",
+                                   "pages_past_table", "row_outside", "shorter_than_prefix"])
+def test_prefix_reports_one_fault(fault):
+    """One bad group or row among healthy ones: ERR_INVALID_ARG, and the healthy groups' rows are
+    right."""
+    c, _ = prefix_cache(99, [3, 3, 4], [5, 9, 2], 2, 64, least=1)
+    q = bf16(c.gen, 10, 4, 64).cuda()
+    ptr, pages, rows = [0, 3, 6, 10], [5, 9, 2], list(range(10))
+    want = K.paged_prefix_attn(q, c.kd, c.vd, c.pool, i32(ptr), i32(pages))
+    good = list(range(3))
+    if fault == "descends":
+        ptr = [0, 3, 6, 5]                          # the last group
+        good = list(range(6))
+    elif fault == "past_batch":
+        ptr, good = [0, 3, 6, 11], list(range(6))
+    elif fault == "below_zero":
+        ptr, good = [-2, 3, 6, 10], list(range(3, 10))
+    elif fault == "pages_negative":
+        pages, good = [5, -3, 2], [0, 1, 2, 6, 7, 8, 9]
+    elif fault == "pages_past_table":
+        pages, good = [5, c.table.shape[1] + 1, 2], [0, 1, 2, 6, 7, 8, 9]
+    elif fault == "row_outside":
+        rows[4], good = 10, [0, 1, 2, 3, 5, 6, 7, 8, 9]
+    else:
+        c.lengths[4], good = 9 * PAGE - 1, [0, 1, 2, 3, 5, 6, 7, 8, 9]
+    status = K.new_status()
+    out = torch.full((10, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    K.paged_prefix_attn(q, c.kd, c.vd, c.make_pool(), i32(ptr), i32(pages), group_rows=i32(rows),
+                        out=out, status=status)
+    assert K.read_status(status) == K.ERR_INVALID_ARG
+    ref, mag = op.dense_attention(H.f64(q), H.f64(c.k), H.f64(c.v), c.table,
+                                  np.where(np.isin(np.arange(10), good), c.lengths, 0), 0.125, PAGE)
+    attention_close(out[good], ref[good], mag[good])
+    attention_close(want[good], ref[good], mag[good])
