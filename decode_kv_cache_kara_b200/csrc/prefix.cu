@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     int len = 0;
     if (j < a.num_groups) {
       const int lo = a.group_ptr[j], hi = a.group_ptr[j + 1], pages = a.prefix_pages[j];
-      if (lo < 0 || hi < lo || hi > a.B || pages < 0 || pages > a.max_blocks) {
+      // an empty group has no pages: what prefix_pages holds for it does not matter
+      if (lo < 0 || hi < lo || hi > a.B || (hi > lo && (pages < 0 || pages > a.max_blocks))) {
         report(a.status, KARA_ERR_INVALID_ARG);
       } else if (hi > lo) {
         gr.first = lo;

@@ -444,7 +444,8 @@ kara_status paged_sparse_attn(const void* q, const void* k_cache, const void* v_
  * Rows in no group are not computed and their out stays as it was. A row listed twice is
  * computed twice. A group may be empty or have one row, and share no page.
  *  group_ptr    device int32 [num_groups + 1], ascending, within [0, batch].
- *  prefix_pages device int32 [num_groups], whole pages (of 16 slots).
+ *  prefix_pages device int32 [num_groups], whole pages (of 16 slots), at most the table's width;
+ *               not used for an empty group.
  *  num_groups   0 .. batch.
  *  group_rows   device int32 [batch] (entries from group_ptr[num_groups] on are not used) or
  *               NULL.

@@ -253,3 +253,17 @@ def test_prefix_reports_one_fault(fault):
                                   np.where(np.isin(np.arange(10), good), c.lengths, 0), 0.125, PAGE)
     attention_close(out[good], ref[good], mag[good])
     attention_close(want[good], ref[good], mag[good])
+
+
+def test_prefix_pages_of_empty_groups_do_not_matter():
+    """A plan of a fixed number of groups: behind and between those in use lie empty ones with any
+    prefix_pages."""
+    c, _ = prefix_cache(100, [3, 4], [5, 2], 2, 64)
+    q = bf16(c.gen, 7, 4, 64)
+    status = K.new_status()
+    out = K.paged_prefix_attn(q.cuda(), c.kd, c.vd, c.pool, i32([0, 0, 3, 3, 7, 7, 7]),
+                              i32([-7, 5, 2 ** 31 - 1, 2, c.table.shape[1] + 1, -2 ** 31]),
+                              status=status)
+    assert K.read_status(status) == 0
+    ref, mag = op.dense_attention(H.f64(q), H.f64(c.k), H.f64(c.v), c.table, c.lengths, 0.125, PAGE)
+    attention_close(out, ref, mag)
