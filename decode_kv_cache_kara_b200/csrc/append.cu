@@ -11,9 +11,9 @@
 // a compression a slot's number is no longer its token's position.
 //
 // Both kernels move every byte once: HBM-bound for prompts and caches, launch latency for a
-// decode step. Measured: 15K prompt tokens of 28 + 2 * 4 heads 48.5 us, 4.9 TB/s (74 % of measured;
-// the sines cost 4 us, the bounds 1 us), one token 3.7 us, 128 tokens 4.4 us; bounds of 580K slots
-// 119 us, 6.2 TB/s (94 %).
+// decode step. Measured: 12.7K prompt tokens of 28 + 2 * 4 heads 48.6 us, 4.85 TB/s (74 % of
+// measured; the sines cost 4 us, the bounds 1 us), one token 3.7 us, 128 tokens 4.4 us; bounds of
+// 636K slots 118 us, 6.2 TB/s (94 %).
 #include <cstdint>
 
 #include "common.cuh"

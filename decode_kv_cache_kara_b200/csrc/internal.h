@@ -24,8 +24,10 @@ int device_slot();
 
 // Launches `kernel` as a programmatic dependent of the previous kernel in `stream`: it may
 // start while that kernel finishes, and it must execute griddepcontrol.wait (which returns once
-// the previous kernel has completed and its memory is visible) before it touches memory.
-// Every library kernel launched this way does so at entry, so stream order holds as usual.
+// the previous kernel has completed and its memory is visible) before it touches memory that
+// the previous kernel writes, or writes memory that it reads. The first kernel of every call does so
+// at entry, and every thread block before it ends, so stream order holds as usual; later kernels of a
+// call may read before their wait what was complete before the kernel in front was let start.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args... args) {

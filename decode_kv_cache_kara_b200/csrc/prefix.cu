@@ -7,6 +7,8 @@
 // streaming decode kernel. Softmax statistics are base 2 and partial results (m, l, o), which
 // join at the end:
 //     m = max m_i,  l = sum 2^(m_i - m) l_i,  out = sum 2^(m_i - m) o_i / l.
+// The weights P are rounded to bf16 (at most 2^-8 of each), the type that the tensor cores take
+// beside bf16 values; l sums the unrounded ones in fp32.
 // Four kernels: plan (groups, rows, the prefix work in units of 128 keys), prefix, stream (the rows'
 // own pages, beside the prefix kernel), join.
 //
@@ -253,8 +255,10 @@ struct PfxSmem {
 // SM's share of HBM. So HBM bounds groups of up to about 128 query rows, products and exponentials larger ones,
 // whose softmax and products alternate between two teams of 128 rows. Rows live in tensor memory:
 // S and P of a row share columns, one thread owns the row, no statistics cross threads.
-// Measured: 128 rows of 28 heads behind 32K slots 76 us, 0.80 PFLOP/s (48 % of measured); 1 to 15
-// rows behind up to 8K slots 48 us, 5.5 TB/s (84 %).
+// Measured: 128 rows of 28 heads behind 32K slots 76 us, 0.79 PFLOP/s (48 % of measured); 16 groups
+// of 3 to 15 rows of 32 heads behind 240 to 7.4K slots 48 us for 195 MB, 4.1 TB/s (62 %): an item of
+// few rows is one team's, whose chain of load, maximum and exponentials is longer than the tile's
+// share of HBM.
 template <int D>
 __global__ void __launch_bounds__(kPfxThreads, 1)
 prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_k,

@@ -14,7 +14,7 @@
 //           near the border, and those are scored again in fp64.
 //   attend  the streaming kernel over the chosen pages, and its join (stream.cu).
 // 128 sequences of 2K to 16K slots, 28 query and 4 KV heads, 128 pages each: score 30 us (147 MB,
-// 75 % of measured HBM), select 17 us, attend 97 us, join 7 us (from cold caches).
+// 75 % of measured HBM), select 17 us, attend 95 to 98 us, join 7 us (from cold caches).
 #include <algorithm>
 #include <cstdint>
 
@@ -357,12 +357,13 @@ __device__ __forceinline__ void clear_extremes(SelectSmem<THREADS>& s) {
   __syncthreads();
 }
 
-// Error of an fp32 score, relative to the sum of its terms' magnitudes (e). A tensor-core step
-// adds 16 exact products to the sum so far and drops bits below 2^-23 of the largest of the 17
-// numbers, at most 17 * 2^-23 of it; over the four steps of a chain that is at most 68 * 2^-23 of
-// the chain's e, over all chains 2^-16.9 e. The fp32 additions of the at most 4 chains are off by
-// 2^-24 of partial sums below e each. e itself is summed in one chain, low by at most 2^-14 of
-// its value. (Measured worst 2^-20.)
+// Error of an fp32 score, relative to the sum of its terms' magnitudes (e). It assumes that a
+// tensor-core step adds 16 exact products to the sum so far and drops at most the bits below 2^-23
+// of the largest of the 17 numbers, at most 17 * 2^-23 of it (how the hardware adds is not
+// specified; the measured worst error, 2^-20 e, leaves a factor of 16). Over the four steps of a
+// chain that is at most 68 * 2^-23 of the chain's e, over all chains 2^-16.9 e. The fp32 additions
+// of the at most 4 chains are off by 2^-24 of partial sums below e each. e itself is summed in one
+// chain, low by at most 2^-14 of its value.
 constexpr float kScoreErr = 1.0f / 65536.0f;
 
 // The largest of the group's exact scores of one page (a warp's work, every lane gets it). Four
@@ -416,7 +417,9 @@ __device__ __forceinline__ double exact_score(const SparseArgs& a, int b, int g,
 // What bounds it is latency: about 15 dependent steps (a load, a barrier, a first fetch of code
 // each), 5 us for a row of 250 pages. 1024 threads where every block has an SM to itself and rows
 // can be long (one sequence of 4K pages: its call 27.6 -> 25.3 us), else 512 (512 rows of 600 pages
-// 149 us against 158 with 1024 and 148 with 256; 32 sequences of 257 pages 34.5, 35.1 and 34.1).
+// 149 us, with 1024 threads 158; 32 sequences of 257 pages 34.5 and 35.1; 256 threads gave 148 and
+// 34.1, no more apart from 512 than two runs are). How long rows are only the device knows: the
+// table's width bounds it, so a wide table takes 1024 threads for short rows too.
 template <int D, int THREADS>
 __global__ void __launch_bounds__(THREADS) page_select_kernel(const SparseArgs a) {
   __shared__ SelectSmem<THREADS> s;

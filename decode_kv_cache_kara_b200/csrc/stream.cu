@@ -7,10 +7,14 @@
 // work differs: the call's pages are one line per KV head, cut into equal ranges, and a warp
 // carries (m, l, o) along its range as long as the row stays the same. All warps finish
 // together whatever the rows' lengths, and a row leaves about as many partials as ranges touch
-// it (fixed 8-page units left 32 page times for the busiest warp where ranges leave 28, and
-// three times the partials, on 128 rows of 128 selected pages). HBM-bound: that case reads its
-// 537 MB in 97 us, 5.5 TB/s (84 % of measured). Taking ranges from a counter as warps become free
-// (2 to 6 per warp) was 3 to 10 % slower than one each.
+// it (128 rows of 128 selected pages and 4 KV heads on the 1776 warps of 148 SMs: fixed 8-page
+// units would give the busiest warp 40 pages and a row 16 partials, ranges give 37 and 4 to 5).
+// HBM-bound: that case reads its 537 MB in 95 to 98 us, 5.5 TB/s (84 % of measured). Taking ranges
+// from a counter as warps become free (2 to 6 per warp) was 3 to 10 % slower than one each.
+//
+// The weights are rounded to bf16 for their product with V (at most 2^-8 of each), the type that
+// the tensor cores take beside bf16 values and that of the dense decode kernel; the sums that divide
+// the output are those of the unrounded weights, in fp32 as scores, maxima and outputs are.
 #include <cuda.h>
 
 #include <algorithm>

@@ -411,6 +411,8 @@ kara_status paged_page_bounds(const void* k_cache, const kara_pool* pool,
  * scores, ties to the lower page. Then, over the slots t of the selected pages P[b][g]:
  *     out[b][h] = sum_t softmax_t( q[b][h] . K[t][g(h)] * scale ) V[t][g(h)],
  *                 t < ctx_len[b] + new_slots.
+ * The weights are rounded to bf16 for their product with V, as in paged_decode_attn; scores, maxima
+ * and sums are fp32.
  *  q, out     bf16 [batch, num_q_heads, head_dim]; an empty context gives a zero row.
  *  bounds     as from paged_page_bounds, for every complete page; finite.
  *  scale      > 0.      num_pages >= 1; sink_pages >= 0, recent_pages >= 1, their sum at most
@@ -438,7 +440,8 @@ kara_status paged_sparse_attn(const void* q, const void* k_cache, const void* v_
  *
  *     out[b][h] = sum_t softmax_t( q[b][h] . K[t][g(h)] * scale ) V[t][g(h)],
  *                 t < ctx_len[b] + new_slots
- * as paged_decode_attn. Group j is the rows group_rows[i] (or i itself when group_rows is NULL),
+ * as paged_decode_attn, the weights rounded to bf16 for their product with V, scores, maxima and
+ * sums in fp32. Group j is the rows group_rows[i] (or i itself when group_rows is NULL),
  * group_ptr[j] <= i < group_ptr[j+1]; their first prefix_pages[j] pages are the same ones and
  * are read through the table row of the group's first row, the rest through each row's own.
  * Rows in no group are not computed and their out stays as it was. A row listed twice is
