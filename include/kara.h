@@ -445,7 +445,8 @@ kara_status paged_sparse_attn(const void* q, const void* k_cache, const void* v_
  * group_ptr[j] <= i < group_ptr[j+1]; their first prefix_pages[j] pages are the same ones and
  * are read through the table row of the group's first row, the rest through each row's own.
  * Rows in no group are not computed and their out stays as it was. A row listed twice is
- * computed twice. A group may be empty or have one row, and share no page.
+ * computed twice, and its out holds values of either (they may differ in the last bits). A group
+ * may be empty or have one row, and share no page.
  *  group_ptr    device int32 [num_groups + 1], ascending, within [0, batch].
  *  prefix_pages device int32 [num_groups], whole pages (of 16 slots), at most the table's width;
  *               not used for an empty group.
